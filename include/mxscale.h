@@ -190,6 +190,130 @@ int mx_last_cuda_error(void);
 /* Library version, major * 10000 + minor * 100 + patch. */
 int mx_version(void);
 
+/* ---------------------------------------------------------------------------
+ * Mixture-of-experts operators around the scales: slots sorted by expert,
+ * token rows into expert order and back, 8-bit quantization, and the grouped
+ * 8-bit product that reads both kinds of scales.
+ *
+ * A slot is one (token, choice) pair, slot = token * choices + choice.  The
+ * rows of all experts follow one another, expert by expert, and each expert's
+ * in the order of their slots; group_ends (int32[num_experts], cumulative) are
+ * the group ends of every entry point here, clamped like group_end_offsets
+ * above.  Slots whose expert id is outside [0, num_experts) have no row (an
+ * expert of another rank): the rows behind the last group belong to nobody and
+ * are written as zeros.  Indexes in device memory that are out of range are
+ * skipped, never followed.
+ *
+ * Strides are in elements.  Outputs must not overlap inputs.  Streams, graphs,
+ * contexts and the bounded waits are as described above.  Any alignment and
+ * stride is taken; rows that start on 16-byte boundaries are moved 16 bytes at
+ * a time, others one element at a time.  The product alone asks for 16-byte
+ * aligned operand rows. */
+typedef enum { MX_F32 = 0, MX_BF16 = 1, MX_F16 = 2, MX_E4M3 = 3, MX_E5M2 = 4 } mx_dtype;
+
+/* Bytes of workspace that mx_expert_sort needs (0 for few slots). Host-only. */
+size_t mx_expert_sort_workspace(int64_t tokens, int32_t choices);
+
+/* Sorts slots by expert, stable.
+ *   expert_ids   device, int32 or int64 (id_bytes 4 or 8) [tokens, choices]
+ *   group_ends   out, int32[num_experts], num_experts 1..64
+ *   row_of_slot  out, int32[tokens * choices]: the slot's row, -1 if it has none
+ *   slot_of_row  out, int32[tokens * choices]: the row's slot, -1 behind the last group
+ *   workspace    device, 4-byte aligned; of one call at a time (two streams, or two
+ *                captured graphs that may run at once, need one each) */
+mx_status mx_expert_sort(const void *expert_ids, int32_t id_bytes, int64_t tokens, int32_t choices, int32_t num_experts,
+                         int32_t *group_ends, int32_t *row_of_slot, int32_t *slot_of_row, void *workspace,
+                         cudaStream_t stream);
+
+/* out[row_of_slot[t, j]] = x[t] for tokens * choices rows of out (f32, bf16 or
+ * f16).  Its gradient is mx_combine_rows without weights. */
+mx_status mx_dispatch_rows(const void *x, mx_dtype dtype, int64_t tokens, int64_t cols, int64_t x_stride,
+                           const int32_t *row_of_slot, int32_t choices, const int32_t *group_ends, int32_t num_experts,
+                           void *out, int64_t out_stride, cudaStream_t stream);
+
+/* y[t] = sum over j of weights[t, j] * rows[row_of_slot[t, j]], over slots that
+ * have a row, in the order of j, in 32 bits, rounded once; weights float32
+ * [tokens, choices], or NULL for ones. */
+mx_status mx_combine_rows(const void *rows, mx_dtype dtype, int64_t tokens, int64_t cols, int64_t rows_stride,
+                          const int32_t *row_of_slot, int32_t choices, const float *weights, void *y, int64_t y_stride,
+                          cudaStream_t stream);
+
+/* Gradient of mx_combine_rows: d_rows[row_of_slot[t, j]] = weights[t, j] * grad[t]
+ * and d_weights[t, j] = <grad[t], rows[row_of_slot[t, j]]> (0 for slots without a row). */
+mx_status mx_combine_rows_backward(const void *grad, mx_dtype dtype, int64_t tokens, int64_t cols, int64_t grad_stride,
+                                   const void *rows, int64_t rows_stride, const int32_t *row_of_slot, int32_t choices,
+                                   const int32_t *group_ends, int32_t num_experts, const float *weights, void *d_rows,
+                                   int64_t d_rows_stride, float *d_weights, cudaStream_t stream);
+
+/* 8-bit values q (e4m3 or e5m2) and E8M0 scales: the scale of a block is the
+ * smallest power of two with which nothing in the block saturates, at least
+ * 2^-127 (byte 0, also that of a block of zeros); q is rounded to nearest, ties
+ * to even.  A block that holds a NaN or an infinity gets the scale byte 255 and
+ * NaN values.
+ *
+ * Rows: blocks of `block` (128 or 32) consecutive columns of a row; the scale of
+ * block i of row r at scales[r * scale_row_stride + i * scale_block_stride].
+ * With row_of_slot (else NULL, and choices, group_ends, num_experts unused)
+ * row t is quantized once and written to the rows row_of_slot[t, :] of q and
+ * scales: mx_dispatch_rows and quantization in one pass. */
+mx_status mx_quantize_rows(const void *x, mx_dtype dtype, int64_t rows, int64_t cols, int64_t x_stride, int32_t block,
+                           mx_dtype out_dtype, const int32_t *row_of_slot, int32_t choices, const int32_t *group_ends,
+                           int32_t num_experts, uint8_t *q, int64_t q_stride, uint8_t *scales, int64_t scale_row_stride,
+                           int64_t scale_block_stride, cudaStream_t stream);
+
+/* Rows that mx_quantize_cols writes: roundup(rows, 128) + 128 * num_groups.  Host-only; 0 for invalid arguments. */
+int64_t mx_padded_rows(int64_t rows, int32_t num_groups);
+
+/* Columns: blocks of 128 consecutive rows of a group in one column.  Group g
+ * starts at row P_g (a multiple of 128, see mx_padded_group_starts) of q; rows
+ * of q that hold no data are zeros.  q is mx_padded_rows(...) x cols, the scale
+ * of rows [128 i, 128 i + 128) of column c at scales[i * scale_stride + c]. */
+mx_status mx_quantize_cols(const void *x, mx_dtype dtype, int64_t rows, int64_t cols, int64_t x_stride,
+                           const int32_t *group_ends, int32_t num_groups, mx_dtype out_dtype, uint8_t *q, int64_t q_stride,
+                           uint8_t *scales, int64_t scale_stride, cudaStream_t stream);
+
+/* Square blocks of 128 x 128 of `groups` matrices; scales are contiguous,
+ * [groups, roundup(rows, 128) / 128, roundup(cols, 128) / 128]. */
+mx_status mx_quantize_blocks(const void *x, mx_dtype dtype, int64_t groups, int64_t rows, int64_t cols, int64_t x_group_stride,
+                             int64_t x_stride, mx_dtype out_dtype, uint8_t *q, int64_t q_group_stride, int64_t q_stride,
+                             uint8_t *scales, cudaStream_t stream);
+
+/* How the weights of a grouped product lie in memory. */
+typedef enum { MX_B_NK = 0, MX_B_KN = 1 } mx_b_layout;
+
+/* Grouped product, groups along the rows (forward, and the input gradient):
+ *   out[r, n] = sum_k a[r, k] * b[g(r), n, k], each value times its scale,
+ * accumulated in 32 bits by the tensor cores.  rows of a behind the last group
+ * give rows of zeros.  a and b are e4m3 or e5m2 (each its own), 16-byte aligned
+ * with row (and, of b, group) strides that are multiples of 16; out is f32,
+ * bf16 or f16.
+ *   b_layout  MX_B_NK: b is [G, n, k]; MX_B_KN: b is [G, k, n], the forward
+ *             weights as they are stored, read for the gradient of the input
+ *   block 128 a's scales cover 128 values of a row (a_scales[r * row_stride +
+ *             i * block_stride]); b's cover 128 x 128 (b_scales[g * group_stride +
+ *             (n / 128) * n_stride + (k / 128) * k_stride])
+ *   block 32  both scales lie in the blocked layout, 16-byte aligned, strides
+ *             unused: a's as mx_rearrange_m_groups writes [rows, k / 32] for
+ *             group_ends, b's as it writes [G * n, k / 32] for groups of n rows;
+ *             MX_B_NK only */
+mx_status mx_grouped_matmul_m(const void *a, mx_dtype a_dtype, int64_t a_stride, const uint8_t *a_scales,
+                              int64_t a_scale_row_stride, int64_t a_scale_block_stride, const void *b, mx_dtype b_dtype,
+                              mx_b_layout b_layout, int64_t b_group_stride, int64_t b_stride, const uint8_t *b_scales,
+                              int64_t b_scale_group_stride, int64_t b_scale_n_stride, int64_t b_scale_k_stride,
+                              int32_t block, int64_t rows, int64_t n, int64_t k, const int32_t *group_ends,
+                              int32_t num_groups, void *out, mx_dtype out_dtype, int64_t out_stride, cudaStream_t stream);
+
+/* Grouped product, groups along the contraction (the weight gradient):
+ *   out[g, m, n] = sum over the rows r of group g of a[r, m] * b[r, n]
+ * with a [padded_rows, m] and b [padded_rows, n] and their scales as
+ * mx_quantize_cols lays them out (groups at padded starts, zeros between).
+ * group_ends are the ends without padding.  A group without rows gives zeros. */
+mx_status mx_grouped_matmul_k(const void *a, mx_dtype a_dtype, int64_t a_stride, const uint8_t *a_scales,
+                              int64_t a_scale_stride, const void *b, mx_dtype b_dtype, int64_t b_stride,
+                              const uint8_t *b_scales, int64_t b_scale_stride, int64_t padded_rows, int64_t m, int64_t n,
+                              const int32_t *group_ends, int32_t num_groups, void *out, mx_dtype out_dtype,
+                              int64_t out_group_stride, int64_t out_stride, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,5 +1,6 @@
 """scale_factor_layout_b200 -- MXFP8 E8M0 scale factors -> per-group 128x4
-blocked layout, on NVIDIA B200 (sm_100a).
+blocked layout, on NVIDIA B200 (sm_100a), and the mixture-of-experts operators
+around them (``moe``: sort by expert, dispatch, combine, quantize, grouped product).
 
 The work runs in libmxscale.so (C ABI in include/mxscale.h); this package is
 its binding.  ``_binding`` mirrors the C entry points one for one (raw
@@ -17,12 +18,29 @@ from ._binding import (  # noqa: F401
     mx_version, status_string,
 )
 
+_MOE = (
+    "ExpertOrder", "expert_sort", "dispatch_rows", "combine_rows", "combine_rows_backward", "quantize_rows",
+    "quantize_cols", "quantize_blocks", "grouped_matmul", "grouped_matmul_k",
+)
+
 __all__ = [
+    *_MOE,
     "rearrange_m_groups", "rearrange_k_groups", "rearrange", "rearranged_size",
     "mx_rearrange_m_groups", "mx_rearrange_k_groups", "mx_rearrange_ex", "mx_rearranged_size",
     "mx_select_path", "mx_device_flags", "mx_version", "MxError", "unrearrange", "padded_group_starts",
     "mx_unrearrange_m_groups", "mx_unrearrange_k_groups", "mx_padded_group_starts",
 ]
+
+
+def __getattr__(name):
+    """The operators of ``moe``, whose module needs torch, at their first use."""
+    if name in _MOE:
+        from . import moe
+
+        for n in _MOE:
+            globals()[n] = getattr(moe, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def rearranged_size(dim: int, rows: int, cols: int, num_groups: int) -> int:

@@ -23,6 +23,10 @@ PATHS = {"auto": MX_PATH_AUTO, "tma": MX_PATH_TMA, "word": MX_PATH_WORD, "byte":
          "flat": MX_PATH_FLAT}
 PATH_NAMES = {v: k for k, v in PATHS.items()}
 
+MX_F32, MX_BF16, MX_F16, MX_E4M3, MX_E5M2 = range(5)
+MX_B_NK, MX_B_KN = 0, 1
+B_LAYOUTS = {"nk": MX_B_NK, "kn": MX_B_KN}
+
 _lock = threading.Lock()
 _lib = None
 
@@ -40,6 +44,24 @@ _SIGNATURES = {
     "mx_unrearrange_m_groups": (ctypes.c_int, [_P, _I64, _I64, _P, _I32, _P, _I64, _P]),
     "mx_unrearrange_k_groups": (ctypes.c_int, [_P, _I64, _I64, _P, _I32, _P, _I64, _P]),
     "mx_padded_group_starts": (ctypes.c_int, [ctypes.c_int, _I64, _I64, _P, _I32, _P, _P]),
+    "mx_expert_sort_workspace": (ctypes.c_size_t, [_I64, _I32]),
+    "mx_expert_sort": (ctypes.c_int, [_P, _I32, _I64, _I32, _I32, _P, _P, _P, _P, _P]),
+    "mx_dispatch_rows": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, _I32, _P, _I32, _P, _I64, _P]),
+    "mx_combine_rows": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, _I32, _P, _P, _I64, _P]),
+    "mx_combine_rows_backward": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, _I64, _P, _I32, _P, _I32, _P,
+                                                _P, _I64, _P, _P]),
+    "mx_quantize_rows": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _I32, ctypes.c_int, _P, _I32, _P, _I32, _P,
+                                        _I64, _P, _I64, _I64, _P]),
+    "mx_padded_rows": (_I64, [_I64, _I32]),
+    "mx_quantize_cols": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, _I32, ctypes.c_int, _P, _I64, _P, _I64,
+                                        _P]),
+    "mx_quantize_blocks": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _I64, _I64, ctypes.c_int, _P, _I64, _I64,
+                                          _P, _P]),
+    "mx_grouped_matmul_m": (ctypes.c_int, [_P, ctypes.c_int, _I64, _P, _I64, _I64, _P, ctypes.c_int, ctypes.c_int, _I64,
+                                           _I64, _P, _I64, _I64, _I64, _I32, _I64, _I64, _I64, _P, _I32, _P,
+                                           ctypes.c_int, _I64, _P]),
+    "mx_grouped_matmul_k": (ctypes.c_int, [_P, ctypes.c_int, _I64, _P, _I64, _P, ctypes.c_int, _I64, _P, _I64, _I64,
+                                           _I64, _I64, _P, _I32, _P, ctypes.c_int, _I64, _I64, _P]),
     "mx_last_cuda_error": (ctypes.c_int, []),
     "mx_version": (ctypes.c_int, []),
 }
@@ -140,3 +162,76 @@ def mx_last_cuda_error() -> int:
 
 def mx_version() -> int:
     return int(lib().mx_version())
+
+
+def mx_expert_sort_workspace(tokens: int, choices: int) -> int:
+    return int(lib().mx_expert_sort_workspace(tokens, choices))
+
+
+def mx_expert_sort(expert_ids: int, id_bytes: int, tokens: int, choices: int, num_experts: int, group_ends: int,
+                   row_of_slot: int, slot_of_row: int, workspace: int, stream: int) -> int:
+    return lib().mx_expert_sort(expert_ids, id_bytes, tokens, choices, num_experts, group_ends, row_of_slot,
+                                slot_of_row, workspace, stream)
+
+
+def mx_dispatch_rows(x: int, dtype: int, tokens: int, cols: int, x_stride: int, row_of_slot: int, choices: int,
+                     group_ends: int, num_experts: int, out: int, out_stride: int, stream: int) -> int:
+    return lib().mx_dispatch_rows(x, dtype, tokens, cols, x_stride, row_of_slot, choices, group_ends, num_experts, out,
+                                  out_stride, stream)
+
+
+def mx_combine_rows(rows: int, dtype: int, tokens: int, cols: int, rows_stride: int, row_of_slot: int, choices: int,
+                    weights: int, y: int, y_stride: int, stream: int) -> int:
+    return lib().mx_combine_rows(rows, dtype, tokens, cols, rows_stride, row_of_slot, choices, weights, y, y_stride,
+                                 stream)
+
+
+def mx_combine_rows_backward(grad: int, dtype: int, tokens: int, cols: int, grad_stride: int, rows: int,
+                             rows_stride: int, row_of_slot: int, choices: int, group_ends: int, num_experts: int,
+                             weights: int, d_rows: int, d_rows_stride: int, d_weights: int, stream: int) -> int:
+    return lib().mx_combine_rows_backward(grad, dtype, tokens, cols, grad_stride, rows, rows_stride, row_of_slot,
+                                          choices, group_ends, num_experts, weights, d_rows, d_rows_stride, d_weights,
+                                          stream)
+
+
+def mx_quantize_rows(x: int, dtype: int, rows: int, cols: int, x_stride: int, block: int, out_dtype: int,
+                     row_of_slot: int, choices: int, group_ends: int, num_experts: int, q: int, q_stride: int,
+                     scales: int, scale_row_stride: int, scale_block_stride: int, stream: int) -> int:
+    return lib().mx_quantize_rows(x, dtype, rows, cols, x_stride, block, out_dtype, row_of_slot, choices, group_ends,
+                                  num_experts, q, q_stride, scales, scale_row_stride, scale_block_stride, stream)
+
+
+def mx_padded_rows(rows: int, num_groups: int) -> int:
+    return int(lib().mx_padded_rows(rows, num_groups))
+
+
+def mx_quantize_cols(x: int, dtype: int, rows: int, cols: int, x_stride: int, group_ends: int, num_groups: int,
+                     out_dtype: int, q: int, q_stride: int, scales: int, scale_stride: int, stream: int) -> int:
+    return lib().mx_quantize_cols(x, dtype, rows, cols, x_stride, group_ends, num_groups, out_dtype, q, q_stride,
+                                  scales, scale_stride, stream)
+
+
+def mx_quantize_blocks(x: int, dtype: int, groups: int, rows: int, cols: int, x_group_stride: int, x_stride: int,
+                       out_dtype: int, q: int, q_group_stride: int, q_stride: int, scales: int, stream: int) -> int:
+    return lib().mx_quantize_blocks(x, dtype, groups, rows, cols, x_group_stride, x_stride, out_dtype, q,
+                                    q_group_stride, q_stride, scales, stream)
+
+
+def mx_grouped_matmul_m(a: int, a_dtype: int, a_stride: int, a_scales: int, a_scale_row_stride: int,
+                        a_scale_block_stride: int, b: int, b_dtype: int, b_layout: int, b_group_stride: int,
+                        b_stride: int, b_scales: int, b_scale_group_stride: int, b_scale_n_stride: int,
+                        b_scale_k_stride: int, block: int, rows: int, n: int, k: int, group_ends: int,
+                        num_groups: int, out: int, out_dtype: int, out_stride: int, stream: int) -> int:
+    return lib().mx_grouped_matmul_m(a, a_dtype, a_stride, a_scales, a_scale_row_stride, a_scale_block_stride, b,
+                                     b_dtype, b_layout, b_group_stride, b_stride, b_scales, b_scale_group_stride,
+                                     b_scale_n_stride, b_scale_k_stride, block, rows, n, k, group_ends, num_groups,
+                                     out, out_dtype, out_stride, stream)
+
+
+def mx_grouped_matmul_k(a: int, a_dtype: int, a_stride: int, a_scales: int, a_scale_stride: int, b: int, b_dtype: int,
+                        b_stride: int, b_scales: int, b_scale_stride: int, padded_rows: int, m: int, n: int,
+                        group_ends: int, num_groups: int, out: int, out_dtype: int, out_group_stride: int,
+                        out_stride: int, stream: int) -> int:
+    return lib().mx_grouped_matmul_k(a, a_dtype, a_stride, a_scales, a_scale_stride, b, b_dtype, b_stride, b_scales,
+                                     b_scale_stride, padded_rows, m, n, group_ends, num_groups, out, out_dtype,
+                                     out_group_stride, out_stride, stream)

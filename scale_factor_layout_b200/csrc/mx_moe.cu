@@ -1,0 +1,517 @@
+// mx_moe.cu -- tokens sorted by expert and back, on B200 (sm_100a): the sort
+// of (token, choice) slots by expert, the copy of token rows into expert
+// order, and the weighted sum of a token's rows with its gradient.
+//
+// All of it is bound by memory (the sort, for few tokens, by latency).  The
+// row kernels go by token, not by sorted row: a token's row is then read once
+// from HBM and written `choices` times (dispatch), or its `choices` rows are
+// read and one written (combine); by sorted row a token's row would be read
+// `choices` times, far apart.  Sums run in 32 bits in the order of a token's
+// choices, with no atomics, so every call gives the same bits.
+
+#include <climits>
+
+#include "mx_ops.cuh"
+
+namespace mx {
+namespace {
+
+// ------------------------------------------------------------------ sort
+// A stable counting sort of S slots by expert (E <= 64).  A CTA takes one
+// contiguous range of slots, each of its warps a contiguous part of that, 32
+// slots a step.  Within a step match_any gives each slot the lanes with the
+// same expert: the slot's rank is the number of lower ones among them.
+//   count:  per-warp counters, then (several CTAs) the CTA's sums to `counts`;
+//   place:  a slot's row = expert's start + earlier CTAs + earlier warps +
+//           earlier steps + rank in the step.
+// One CTA does both in one launch up to kSortOneCta slots; above, two
+// launches, because a CTA needs the counts of all earlier ones.
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int64_t kSortOneCta = 8192;
+constexpr int64_t kSortChunk = 2048;   // slots of a CTA, at least
+constexpr int kSortMaxCtas = 148;
+
+template <typename Id>
+__device__ __forceinline__ int load_expert(const Id *ids, int64_t s, int64_t end, int E) {
+    if (s >= end) return -1;
+    const Id v = ids[s];
+    return v >= 0 && v < (Id)E ? (int)v : -1;
+}
+
+struct SortShared {
+    int warp[kSortWarps][kMaxGroups + 1]; // counts, then next row of the warp's slots
+    int total[kMaxGroups];              // the CTA's counts
+    int before[kMaxGroups];             // counts of earlier CTAs
+    int all[kMaxGroups];                // counts of all CTAs
+    int start[kMaxGroups + 1];
+};
+
+// Per-warp counts of slots [begin, end) in sh.warp.
+template <typename Id>
+__device__ __forceinline__ void sort_count(const Id *ids, int64_t begin, int64_t end, int64_t per_warp, int E,
+                                           SortShared &sh) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    sh.warp[w][lane] = 0;
+    sh.warp[w][lane + 32] = 0;
+    __syncwarp();
+    const int64_t from = begin + w * per_warp, to = min(end, from + per_warp);
+    for (int64_t at = from; at < to; at += 32) {
+        const int e = load_expert(ids, at + lane, to, E);
+        const unsigned same = __match_any_sync(0xffffffffu, e);
+        if (e >= 0 && lane == __ffs(same) - 1) sh.warp[w][e] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+}
+
+// Warp w turns the per-warp counts of experts w and w + 32 into exclusive sums
+// over the warps, and leaves the CTA's count in sh.total.
+__device__ __forceinline__ void sort_scan_warps(SortShared &sh) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int e = w + 32 * h;
+        const int n = sh.warp[lane][e];
+        const int sum = warp_scan_sum(n, lane);
+        sh.warp[lane][e] = sum - n;
+        if (lane == 31) sh.total[e] = sum;
+    }
+    __syncthreads();
+}
+
+template <typename Id>
+__global__ void __launch_bounds__(kSortThreads)
+sort_count_kernel(const Id *__restrict__ ids, int64_t S, int64_t per_cta, int64_t per_warp, int E, int *__restrict__ counts) {
+    __shared__ SortShared sh;
+    grid_dependency_wait();
+    const int64_t begin = blockIdx.x * per_cta, end = min(S, begin + per_cta);
+    sort_count(ids, begin, end, per_warp, E, sh);
+    sort_scan_warps(sh);
+    if (threadIdx.x < kMaxGroups) counts[blockIdx.x * kMaxGroups + threadIdx.x] = sh.total[threadIdx.x];
+}
+
+template <typename Id>
+__global__ void __launch_bounds__(kSortThreads)
+sort_place_kernel(const Id *__restrict__ ids, int64_t S, int64_t per_cta, int64_t per_warp, int E,
+                  const int *__restrict__ counts, int *__restrict__ group_ends, int *__restrict__ row_of_slot,
+                  int *__restrict__ slot_of_row) {
+    __shared__ SortShared sh;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    grid_dependency_wait();
+    const int64_t begin = blockIdx.x * per_cta, end = min(S, begin + per_cta);
+    if (tid < kMaxGroups) sh.before[tid] = sh.all[tid] = 0;
+    sort_count(ids, begin, end, per_warp, E, sh);
+    sort_scan_warps(sh);
+    if (counts != nullptr) {
+        // 16 threads an expert add up the CTAs' counts
+        const int e = tid & (kMaxGroups - 1);
+        int before = 0, all = 0;
+        for (int b = tid / kMaxGroups; b < (int)gridDim.x; b += kSortThreads / kMaxGroups) {
+            const int n = counts[b * kMaxGroups + e];
+            all += n;
+            if (b < (int)blockIdx.x) before += n;
+        }
+        atomicAdd(&sh.before[e], before);   // whole numbers: the order does not matter
+        atomicAdd(&sh.all[e], all);
+    } else if (tid < kMaxGroups) {
+        sh.all[tid] = sh.total[tid];
+    }
+    __syncthreads();
+    if (w == 0) {
+        const int n0 = sh.all[lane], n1 = sh.all[lane + 32];
+        const int s0 = warp_scan_sum(n0, lane);
+        const int s1 = warp_scan_sum(n1, lane) + __shfl_sync(0xffffffffu, s0, 31);
+        sh.start[lane] = s0 - n0;
+        sh.start[lane + 32] = s1 - n1;
+        if (lane == 31) sh.start[kMaxGroups] = s1;
+        if (blockIdx.x == 0) {
+            if (lane < E) group_ends[lane] = s0;
+            if (lane + 32 < E) group_ends[lane + 32] = s1;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int e = lane + 32 * h;
+        sh.warp[w][e] += sh.start[e] + sh.before[e];
+    }
+    __syncwarp();
+    const int64_t from = begin + w * per_warp, to = min(end, from + per_warp);
+    for (int64_t at = from; at < to; at += 32) {
+        const int e = load_expert(ids, at + lane, to, E);
+        const unsigned same = __match_any_sync(0xffffffffu, e);
+        int row = -1;
+        if (e >= 0) row = sh.warp[w][e] + __popc(same & ((1u << lane) - 1u));
+        __syncwarp();
+        if (e >= 0 && lane == __ffs(same) - 1) sh.warp[w][e] += __popc(same);
+        __syncwarp();
+        if (at + lane < to) {
+            row_of_slot[at + lane] = row;
+            if (row >= 0) slot_of_row[row] = (int)(at + lane);
+        }
+    }
+    // rows behind the last group
+    for (int64_t r = sh.start[kMaxGroups] + (int64_t)blockIdx.x * kSortThreads + tid; r < S;
+         r += (int64_t)gridDim.x * kSortThreads)
+        slot_of_row[r] = -1;
+}
+
+// ------------------------------------------------------------------ rows
+// A CTA of 256 threads takes 256 / tpr tokens and one chunk of tpr packs of
+// their rows (tpr a power of two: the packs of a row, at most 256).  Chunks of
+// a token are neighbours in the grid, so their rows are touched together.
+constexpr int kRowThreads = 256;
+
+struct RowShape {
+    int64_t tokens, rows;   // tokens; rows = tokens * choices
+    int32_t k;              // choices a token
+    int32_t packs;          // packs of a row
+    int32_t tpr_log2;
+    int32_t chunks;
+};
+
+template <typename P>
+__device__ __forceinline__ void zero_rows(P *__restrict__ out, int64_t stride, int64_t from, const RowShape &s) {
+    if (from < 0) from = 0;
+    const int64_t n = (s.rows - from) * s.packs;
+    P zero;
+    memset(&zero, 0, sizeof(zero));
+    for (int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kRowThreads) {
+        const int64_t r = i / s.packs;
+        out[(from + r) * stride + (i - r * s.packs)] = zero;
+    }
+}
+
+// out[row_of_slot[t, j]] = x[t]; rows from *last_end on = 0.  Strides in packs.
+template <typename P>
+__global__ void __launch_bounds__(kRowThreads)
+dispatch_kernel(const P *__restrict__ x, int64_t x_stride, const int *__restrict__ row_of_slot,
+                const int *__restrict__ last_end, P *__restrict__ out, int64_t out_stride, RowShape s) {
+    grid_dependency_wait();
+    const int64_t slab = blockIdx.x / s.chunks;
+    const int chunk = (int)(blockIdx.x - slab * s.chunks);
+    const int64_t t = (slab << (8 - s.tpr_log2)) + (threadIdx.x >> s.tpr_log2);
+    const int p = (chunk << s.tpr_log2) + (threadIdx.x & ((1 << s.tpr_log2) - 1));
+    if (t < s.tokens && p < s.packs) {
+        const P v = x[t * x_stride + p];
+        const int *rows = row_of_slot + t * s.k;
+        for (int j = 0; j < s.k; ++j) {
+            const int64_t r = rows[j];
+            if (r >= 0 && r < s.rows) out[r * out_stride + p] = v;
+        }
+    }
+    zero_rows(out, out_stride, (int64_t)*last_end, s);
+}
+
+// y[t] = sum_j w[t, j] * rows[row_of_slot[t, j]] over the slots that have a row.
+template <typename T, int N>
+__global__ void __launch_bounds__(kRowThreads)
+combine_kernel(const T *__restrict__ rows, int64_t rows_stride, const int *__restrict__ row_of_slot,
+               const float *__restrict__ weights, T *__restrict__ y, int64_t y_stride, RowShape s) {
+    using P = Pack<T, N>;
+    grid_dependency_wait();
+    const int64_t slab = blockIdx.x / s.chunks;
+    const int chunk = (int)(blockIdx.x - slab * s.chunks);
+    const int64_t t = (slab << (8 - s.tpr_log2)) + (threadIdx.x >> s.tpr_log2);
+    const int p = (chunk << s.tpr_log2) + (threadIdx.x & ((1 << s.tpr_log2) - 1));
+    if (t >= s.tokens || p >= s.packs) return;
+    float sum[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum[i] = 0.f;
+    constexpr int kAhead = 8;   // rows whose loads are in flight together
+    for (int j0 = 0; j0 < s.k; j0 += kAhead) {
+        P v[kAhead];
+        float w[kAhead];
+        bool live[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int64_t slot = t * s.k + j0 + u;
+            const int64_t r = j0 + u < s.k ? row_of_slot[slot] : -1;
+            live[u] = r >= 0 && r < s.rows;
+            w[u] = 1.f;
+            if (live[u]) {
+                v[u] = *reinterpret_cast<const P *>(rows + r * rows_stride + (int64_t)p * N);
+                if (weights != nullptr) w[u] = weights[slot];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (live[u]) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) sum[i] = fmaf(w[u], to_f32(v[u].v[i]), sum[i]);
+            }
+    }
+    P o;
+#pragma unroll
+    for (int i = 0; i < N; ++i) o.v[i] = from_f32<T>(sum[i]);
+    *reinterpret_cast<P *>(y + t * y_stride + (int64_t)p * N) = o;
+}
+
+// d_rows[row_of_slot[t, j]] = w[t, j] * grad[t]; d_weights[t, j] = <grad[t], rows[...]>.
+// kTpt threads take one token and walk its whole row, because the inner
+// products run over it: a warp a token for short rows, a CTA for long ones.
+template <typename T, int N, int kTpt>
+__global__ void __launch_bounds__(kRowThreads)
+combine_backward_kernel(const T *__restrict__ grad, int64_t grad_stride, const T *__restrict__ rows,
+                        int64_t rows_stride, const int *__restrict__ row_of_slot, const int *__restrict__ last_end,
+                        const float *__restrict__ weights, T *__restrict__ d_rows, int64_t d_rows_stride,
+                        float *__restrict__ d_weights, RowShape s) {
+    using P = Pack<T, N>;
+    constexpr int kAhead = 8;
+    __shared__ float part[kRowThreads / 32][kAhead];
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int64_t t = (int64_t)blockIdx.x * (kRowThreads / kTpt) + threadIdx.x / kTpt;
+    if (t < s.tokens) {   // the same for all threads of a warp, and of the CTA where it takes one token
+        for (int j0 = 0; j0 < s.k; j0 += kAhead) {
+            int64_t at[kAhead];
+            float wt[kAhead], dot[kAhead];
+            bool live[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int64_t slot = t * s.k + j0 + u;
+                const int64_t r = j0 + u < s.k ? row_of_slot[slot] : -1;
+                live[u] = r >= 0 && r < s.rows;
+                at[u] = r;
+                wt[u] = live[u] ? weights[slot] : 0.f;
+                dot[u] = 0.f;
+            }
+            for (int p = threadIdx.x % kTpt; p < s.packs; p += kTpt) {
+                const P g = *reinterpret_cast<const P *>(grad + t * grad_stride + (int64_t)p * N);
+                P v[kAhead];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u)
+                    if (live[u]) v[u] = *reinterpret_cast<const P *>(rows + at[u] * rows_stride + (int64_t)p * N);
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u)
+                    if (live[u]) {
+                        P o;
+#pragma unroll
+                        for (int i = 0; i < N; ++i) {
+                            const float gi = to_f32(g.v[i]);
+                            dot[u] = fmaf(gi, to_f32(v[u].v[i]), dot[u]);
+                            o.v[i] = from_f32<T>(wt[u] * gi);
+                        }
+                        *reinterpret_cast<P *>(d_rows + at[u] * d_rows_stride + (int64_t)p * N) = o;
+                    }
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], d);
+            }
+            if (kTpt == 32) {
+                if (lane == 0)
+                    for (int u = 0; u < kAhead && j0 + u < s.k; ++u) d_weights[t * s.k + j0 + u] = dot[u];
+            } else {
+                __syncthreads();
+                if (lane == 0) {
+#pragma unroll
+                    for (int u = 0; u < kAhead; ++u) part[w][u] = dot[u];
+                }
+                __syncthreads();
+                if (threadIdx.x < kAhead && j0 + threadIdx.x < s.k) {
+                    float sum = 0.f;
+                    for (int q = 0; q < kRowThreads / 32; ++q) sum += part[q][threadIdx.x];
+                    d_weights[t * s.k + j0 + threadIdx.x] = sum;
+                }
+            }
+        }
+    }
+    RowShape z = s;
+    zero_rows(reinterpret_cast<P *>(d_rows), d_rows_stride / N, (int64_t)*last_end, z);
+}
+
+// ------------------------------------------------------------------ host side
+int64_t sort_ctas(int64_t S) {
+    if (S <= kSortOneCta) return 1;
+    const int64_t n = div_up(S, kSortChunk);
+    return n < kSortMaxCtas ? n : kSortMaxCtas;
+}
+
+bool slots_ok(int64_t tokens, int32_t choices) {
+    return tokens >= 0 && choices >= 1 && tokens <= kOpsMaxExtent && tokens * choices <= kOpsMaxExtent;
+}
+
+int element_bytes(mx_dtype t) {
+    return t == MX_F32 ? 4 : t == MX_BF16 || t == MX_F16 ? 2 : 0;
+}
+
+template <typename Id>
+mx_status sort_typed(const void *ids, int64_t S, int32_t E, int32_t *group_ends, int32_t *row_of_slot,
+                     int32_t *slot_of_row, int32_t *workspace, cudaStream_t stream) {
+    const int64_t ctas = sort_ctas(S);
+    const int64_t per_warp = up_to(div_up(S, ctas * kSortWarps), 32);
+    const int64_t per_cta = per_warp * kSortWarps;
+    const Id *p = static_cast<const Id *>(ids);
+    if (ctas > 1)
+        if (mx_status st = launch(sort_count_kernel<Id>, ctas, kSortThreads, 0, stream, p, S, per_cta, per_warp, E, workspace);
+            st != MX_OK)
+            return st;
+    return launch(sort_place_kernel<Id>, ctas, kSortThreads, 0, stream, p, S, per_cta, per_warp, E,
+                  static_cast<const int *>(ctas > 1 ? workspace : nullptr), group_ends, row_of_slot, slot_of_row);
+}
+
+// Elements of a pack: 16 bytes where every row of every matrix starts on a
+// 16-byte boundary and holds whole packs, one element otherwise.
+struct Mat { const void *p; int64_t stride; };
+template <int n>
+int pack_elements(int es, int64_t cols, const Mat (&m)[n]) {
+    const int N = 16 / es;
+    if (cols % N != 0) return 1;
+    for (const Mat &a : m)
+        if (!aligned_to(a.p, 16) || a.stride % N != 0) return 1;
+    return N;
+}
+
+mx_status row_shape(int64_t tokens, int32_t choices, int64_t packs, RowShape *s, int64_t *grid) {
+    s->tokens = tokens;
+    s->rows = tokens * choices;
+    s->k = choices;
+    s->packs = (int32_t)packs;
+    s->tpr_log2 = 0;
+    while (s->tpr_log2 < 8 && (1 << s->tpr_log2) < packs) ++s->tpr_log2;
+    s->chunks = (int32_t)div_up(packs, 1ll << s->tpr_log2);
+    *grid = div_up(tokens, kRowThreads >> s->tpr_log2) * s->chunks;
+    return *grid > INT_MAX ? MX_ERR_UNSUPPORTED : MX_OK;
+}
+
+template <typename P>
+mx_status dispatch_typed(const void *x, int64_t x_stride, const int32_t *row_of_slot, const int32_t *last_end, void *out,
+                         int64_t out_stride, int64_t tokens, int32_t choices, int64_t packs, cudaStream_t stream) {
+    RowShape s;
+    int64_t grid;
+    if (mx_status st = row_shape(tokens, choices, packs, &s, &grid); st != MX_OK) return st;
+    return launch(dispatch_kernel<P>, grid, kRowThreads, 0, stream, static_cast<const P *>(x), x_stride, row_of_slot,
+                  last_end, static_cast<P *>(out), out_stride, s);
+}
+
+template <typename T, int N>
+mx_status combine_typed(const void *rows, int64_t rows_stride, const int32_t *row_of_slot, const float *weights, void *y,
+                        int64_t y_stride, int64_t tokens, int32_t choices, int64_t cols, cudaStream_t stream) {
+    RowShape s;
+    int64_t grid;
+    if (mx_status st = row_shape(tokens, choices, cols / N, &s, &grid); st != MX_OK) return st;
+    return launch(combine_kernel<T, N>, grid, kRowThreads, 0, stream, static_cast<const T *>(rows), rows_stride,
+                  row_of_slot, weights, static_cast<T *>(y), y_stride, s);
+}
+
+template <typename T, int N>
+mx_status backward_typed(const void *grad, int64_t grad_stride, const void *rows, int64_t rows_stride,
+                         const int32_t *row_of_slot, const int32_t *last_end, const float *weights, void *d_rows,
+                         int64_t d_rows_stride, float *d_weights, int64_t tokens, int32_t choices, int64_t cols,
+                         cudaStream_t stream) {
+    RowShape s;
+    int64_t grid;
+    if (mx_status st = row_shape(tokens, choices, cols / N, &s, &grid); st != MX_OK) return st;
+    const bool warp = s.packs <= 128;
+    const int64_t ctas = warp ? div_up(tokens, kRowThreads / 32) : tokens;
+    return launch(warp ? combine_backward_kernel<T, N, 32> : combine_backward_kernel<T, N, kRowThreads>, ctas,
+                  kRowThreads, 0, stream, static_cast<const T *>(grad), grad_stride, static_cast<const T *>(rows),
+                  rows_stride, row_of_slot, last_end, weights, static_cast<T *>(d_rows), d_rows_stride, d_weights, s);
+}
+
+}  // namespace
+}  // namespace mx
+
+extern "C" {
+
+size_t mx_expert_sort_workspace(int64_t tokens, int32_t choices) {
+    if (!mx::slots_ok(tokens, choices)) return 0;
+    const int64_t ctas = mx::sort_ctas(tokens * choices);
+    return ctas > 1 ? (size_t)(ctas * mx::kMaxGroups * 4) : 0;
+}
+
+mx_status mx_expert_sort(const void *expert_ids, int32_t id_bytes, int64_t tokens, int32_t choices, int32_t num_experts,
+                         int32_t *group_ends, int32_t *row_of_slot, int32_t *slot_of_row, void *workspace,
+                         cudaStream_t stream) {
+    if (!mx::slots_ok(tokens, choices) || num_experts < 1 || num_experts > MX_MAX_GROUPS) return MX_ERR_INVALID_ARG;
+    if (id_bytes != 4 && id_bytes != 8) return MX_ERR_INVALID_ARG;
+    const int64_t S = tokens * choices;
+    if (group_ends == nullptr || (S > 0 && (expert_ids == nullptr || row_of_slot == nullptr || slot_of_row == nullptr)))
+        return MX_ERR_INVALID_ARG;
+    if (mx_expert_sort_workspace(tokens, choices) > 0 && workspace == nullptr) return MX_ERR_INVALID_ARG;
+    if (!mx::aligned_to(expert_ids, id_bytes) || !mx::aligned_to(group_ends, 4) || !mx::aligned_to(row_of_slot, 4) ||
+        !mx::aligned_to(slot_of_row, 4) || !mx::aligned_to(workspace, 4))
+        return MX_ERR_MISALIGNED;
+    int sms = 0;
+    if (mx_status st = mx_device_sms(&sms); st != MX_OK) return st;
+    auto *ws = static_cast<int32_t *>(workspace);
+    return id_bytes == 4 ? mx::sort_typed<int32_t>(expert_ids, S, num_experts, group_ends, row_of_slot, slot_of_row, ws, stream)
+                         : mx::sort_typed<int64_t>(expert_ids, S, num_experts, group_ends, row_of_slot, slot_of_row, ws, stream);
+}
+
+mx_status mx_dispatch_rows(const void *x, mx_dtype dtype, int64_t tokens, int64_t cols, int64_t x_stride,
+                           const int32_t *row_of_slot, int32_t choices, const int32_t *group_ends, int32_t num_experts,
+                           void *out, int64_t out_stride, cudaStream_t stream) {
+    const int es = mx::element_bytes(dtype);
+    if (es == 0 || !mx::slots_ok(tokens, choices) || cols < 0 || cols > mx::kOpsMaxExtent) return MX_ERR_INVALID_ARG;
+    if (num_experts < 1 || num_experts > MX_MAX_GROUPS || x_stride < cols || out_stride < cols) return MX_ERR_INVALID_ARG;
+    if (tokens == 0 || cols == 0) return MX_OK;
+    if (x == nullptr || out == nullptr || row_of_slot == nullptr || group_ends == nullptr) return MX_ERR_INVALID_ARG;
+    if (!mx::aligned_to(x, es) || !mx::aligned_to(out, es) || !mx::aligned_to(row_of_slot, 4) || !mx::aligned_to(group_ends, 4))
+        return MX_ERR_MISALIGNED;
+    int sms = 0;
+    if (mx_status st = mx_device_sms(&sms); st != MX_OK) return st;
+    const int32_t *last = group_ends + num_experts - 1;
+    const mx::Mat mats[] = {{x, x_stride}, {out, out_stride}};
+    const int N = mx::pack_elements(es, cols, mats);
+    if (N > 1)
+        return mx::dispatch_typed<uint4>(x, x_stride / N, row_of_slot, last, out, out_stride / N, tokens, choices, cols / N, stream);
+    return es == 4 ? mx::dispatch_typed<uint32_t>(x, x_stride, row_of_slot, last, out, out_stride, tokens, choices, cols, stream)
+                   : mx::dispatch_typed<uint16_t>(x, x_stride, row_of_slot, last, out, out_stride, tokens, choices, cols, stream);
+}
+
+mx_status mx_combine_rows(const void *rows, mx_dtype dtype, int64_t tokens, int64_t cols, int64_t rows_stride,
+                          const int32_t *row_of_slot, int32_t choices, const float *weights, void *y, int64_t y_stride,
+                          cudaStream_t stream) {
+    const int es = mx::element_bytes(dtype);
+    if (es == 0 || !mx::slots_ok(tokens, choices) || cols < 0 || cols > mx::kOpsMaxExtent) return MX_ERR_INVALID_ARG;
+    if (rows_stride < cols || y_stride < cols) return MX_ERR_INVALID_ARG;
+    if (tokens == 0 || cols == 0) return MX_OK;
+    if (rows == nullptr || y == nullptr || row_of_slot == nullptr) return MX_ERR_INVALID_ARG;
+    if (!mx::aligned_to(rows, es) || !mx::aligned_to(y, es) || !mx::aligned_to(row_of_slot, 4) || !mx::aligned_to(weights, 4))
+        return MX_ERR_MISALIGNED;
+    int sms = 0;
+    if (mx_status st = mx_device_sms(&sms); st != MX_OK) return st;
+    const mx::Mat mats[] = {{rows, rows_stride}, {y, y_stride}};
+    const bool wide = mx::pack_elements(es, cols, mats) > 1;
+#define MX_COMBINE(T, N) mx::combine_typed<T, N>(rows, rows_stride, row_of_slot, weights, y, y_stride, tokens, choices, cols, stream)
+    if (dtype == MX_F32) return wide ? MX_COMBINE(float, 4) : MX_COMBINE(float, 1);
+    if (dtype == MX_BF16) return wide ? MX_COMBINE(__nv_bfloat16, 8) : MX_COMBINE(__nv_bfloat16, 1);
+    return wide ? MX_COMBINE(__half, 8) : MX_COMBINE(__half, 1);
+#undef MX_COMBINE
+}
+
+mx_status mx_combine_rows_backward(const void *grad, mx_dtype dtype, int64_t tokens, int64_t cols, int64_t grad_stride,
+                                   const void *rows, int64_t rows_stride, const int32_t *row_of_slot, int32_t choices,
+                                   const int32_t *group_ends, int32_t num_experts, const float *weights, void *d_rows,
+                                   int64_t d_rows_stride, float *d_weights, cudaStream_t stream) {
+    const int es = mx::element_bytes(dtype);
+    if (es == 0 || !mx::slots_ok(tokens, choices) || cols < 1 || cols > mx::kOpsMaxExtent) return MX_ERR_INVALID_ARG;
+    if (num_experts < 1 || num_experts > MX_MAX_GROUPS) return MX_ERR_INVALID_ARG;
+    if (grad_stride < cols || rows_stride < cols || d_rows_stride < cols) return MX_ERR_INVALID_ARG;
+    if (tokens == 0) return MX_OK;
+    if (grad == nullptr || rows == nullptr || row_of_slot == nullptr || group_ends == nullptr || weights == nullptr ||
+        d_rows == nullptr || d_weights == nullptr)
+        return MX_ERR_INVALID_ARG;
+    if (!mx::aligned_to(grad, es) || !mx::aligned_to(rows, es) || !mx::aligned_to(d_rows, es) ||
+        !mx::aligned_to(row_of_slot, 4) || !mx::aligned_to(group_ends, 4) || !mx::aligned_to(weights, 4) ||
+        !mx::aligned_to(d_weights, 4))
+        return MX_ERR_MISALIGNED;
+    int sms = 0;
+    if (mx_status st = mx_device_sms(&sms); st != MX_OK) return st;
+    const int32_t *last = group_ends + num_experts - 1;
+    const mx::Mat mats[] = {{grad, grad_stride}, {rows, rows_stride}, {d_rows, d_rows_stride}};
+    const bool wide = mx::pack_elements(es, cols, mats) > 1;
+#define MX_BACKWARD(T, N)                                                                                              \
+    mx::backward_typed<T, N>(grad, grad_stride, rows, rows_stride, row_of_slot, last, weights, d_rows, d_rows_stride, \
+                             d_weights, tokens, choices, cols, stream)
+    if (dtype == MX_F32) return wide ? MX_BACKWARD(float, 4) : MX_BACKWARD(float, 1);
+    if (dtype == MX_BF16) return wide ? MX_BACKWARD(__nv_bfloat16, 8) : MX_BACKWARD(__nv_bfloat16, 1);
+    return wide ? MX_BACKWARD(__half, 8) : MX_BACKWARD(__half, 1);
+#undef MX_BACKWARD
+}
+
+}  // extern "C"

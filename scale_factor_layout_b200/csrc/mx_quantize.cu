@@ -1,0 +1,433 @@
+// mx_quantize.cu -- 8-bit floating point with one power-of-two scale (E8M0)
+// for each block of values, on B200 (sm_100a).
+//
+// For a block with largest magnitude A the scale is 2^e, e the smallest whole
+// number with A <= F * 2^e, where F = 1.75 * 2^8 (e4m3) or 1.75 * 2^15 (e5m2)
+// is the type's largest value: nothing saturates.  With A = m * 2^a, 1 <= m < 2,
+// that is e = a - 8 (or 15), plus one if m > 1.75: read off A's bits, with no
+// logarithm.  x * 2^-e is exact in 32 bits wherever it does not vanish, so the
+// only rounding is the one to 8 bits (to nearest, ties to even).  The scale
+// byte is e + 127, at least 0; a block that holds a NaN or an infinity gets
+// the byte 255 (NaN) and NaN elements.  A block of zeros gets the byte 0.
+//
+// Everything here is bound by memory.  A thread holds 8 consecutive elements
+// (one 16-byte load of 16-bit input, one 8-byte store), because a block of
+// 128 is then 16 neighbouring lanes and its maximum 4 shuffles.
+
+#include <climits>
+
+#include <cuda_fp8.h>
+
+#include "mx_ops.cuh"
+
+namespace mx {
+namespace {
+
+constexpr int kQThreads = 256;
+constexpr uint32_t kInfBits = 0x7f800000u;
+
+// Magnitudes are compared as bits: the order of finite values is that of their
+// bits, and infinities and NaNs lie above all of them.
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax, int fexp) {
+    if (amax >= kInfBits) return 255u;
+    const int b = (int)(amax >> 23) - fexp + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return amax < 0x800000u || b < 0 ? 0u : (uint32_t)b;
+}
+
+// 2^-e of a finite scale byte: its exponent field is 254 - byte, 7 .. 254.
+__device__ __forceinline__ float inverse_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+
+__device__ __forceinline__ uint32_t two_eight_bit(float lo, float hi, bool e5m2) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, e5m2 ? __NV_E5M2 : __NV_E4M3);
+}
+
+// Eight values as 8 bytes; 0x7f is a NaN in both types.
+__device__ __forceinline__ uint2 eight_bits(const float (&v)[8], uint32_t byte, bool e5m2) {
+    if (byte == 255u) return make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+    const float s = inverse_scale(byte);
+    uint2 q;
+    q.x = two_eight_bit(v[0] * s, v[1] * s, e5m2) | two_eight_bit(v[2] * s, v[3] * s, e5m2) << 16;
+    q.y = two_eight_bit(v[4] * s, v[5] * s, e5m2) | two_eight_bit(v[6] * s, v[7] * s, e5m2) << 16;
+    return q;
+}
+
+// Eight consecutive elements of a row from column c on, zeros past `cols`.
+// kWide: rows start on 16-byte boundaries and cols is a multiple of 8.
+template <typename T, bool kWide>
+__device__ __forceinline__ Pack<T, 8> load8(const T *row, int c, int cols) {
+    Pack<T, 8> v;
+    if (kWide) {
+        if (c < cols) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(row + c);
+            uint4 *dst = reinterpret_cast<uint4 *>(&v);
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(T) / 2; ++i) dst[i] = __ldg(src + i);
+        } else {
+            memset(&v, 0, sizeof(v));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v.v[i] = c + i < cols ? row[c + i] : from_f32<T>(0.f);
+    }
+    return v;
+}
+
+template <bool kWide>
+__device__ __forceinline__ void store8(uint8_t *row, int c, int cols, uint2 q) {
+    if (kWide) {
+        if (c < cols) *reinterpret_cast<uint2 *>(row + c) = q;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i < cols) row[c + i] = (uint8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
+    }
+}
+
+// ------------------------------------------------------------------ rows
+struct RowsArgs {
+    uint8_t *q;
+    int64_t q_stride;
+    uint8_t *scales;
+    int64_t scale_row, scale_block;   // bytes between the scales of neighbouring rows and blocks
+    const int *row_of_slot;           // kOrder: the rows that each token goes to
+    const int *last_end;
+    int64_t in_rows, out_rows;
+    int32_t cols, k, segments;
+    bool e5m2;
+};
+
+// A CTA takes 32 rows x 256 columns, each warp 4 of the rows (4 loads in
+// flight a lane).  kOrder: row t is written to the rows row_of_slot[t, :], so a
+// token is read and rounded once however many experts it goes to.
+template <typename T, bool kWide, int kBlock, bool kOrder>
+__global__ void __launch_bounds__(kQThreads)
+quantize_rows_kernel(const T *__restrict__ x, int64_t x_stride, RowsArgs a) {
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int64_t band = blockIdx.x / a.segments;
+    const int c = (int)(blockIdx.x - band * a.segments) * 256 + lane * 8;
+    const int64_t r0 = band * 32 + w * 4;
+    const int fexp = a.e5m2 ? 15 : 8;
+    Pack<T, 8> v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (r0 + i < a.in_rows) v[i] = load8<T, kWide>(x + (r0 + i) * x_stride, c, a.cols);
+        else memset(&v[i], 0, sizeof(v[i]));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float f[8];
+        uint32_t amax = 0;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            f[u] = to_f32(v[i].v[u]);
+            amax = max(amax, magnitude(f[u]));
+        }
+#pragma unroll
+        for (int d = 1; d < kBlock / 8; d <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+        const uint32_t byte = scale_byte(amax, fexp);
+        const uint2 q = eight_bits(f, byte, a.e5m2);
+        const int64_t t = r0 + i;
+        if (t < a.in_rows && c < a.cols) {
+            const bool scaler = lane % (kBlock / 8) == 0;
+            const int64_t block_at = (int64_t)(c / kBlock) * a.scale_block;
+            if (!kOrder) {
+                store8<kWide>(a.q + t * a.q_stride, c, a.cols, q);
+                if (scaler) a.scales[t * a.scale_row + block_at] = (uint8_t)byte;
+            } else {
+                for (int j = 0; j < a.k; ++j) {
+                    const int64_t r = a.row_of_slot[t * a.k + j];
+                    if (r < 0 || r >= a.out_rows) continue;
+                    store8<kWide>(a.q + r * a.q_stride, c, a.cols, q);
+                    if (scaler) a.scales[r * a.scale_row + block_at] = (uint8_t)byte;
+                }
+            }
+        }
+    }
+    if (kOrder) {   // rows behind the last group
+        int64_t from = *a.last_end;
+        if (from < 0) from = 0;
+        const int64_t units = (int64_t)a.segments * 32, n = (a.out_rows - from) * units;
+        for (int64_t i = (int64_t)blockIdx.x * kQThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kQThreads) {
+            const int64_t r = from + i / units;
+            const int at = (int)(i % units) * 8;
+            store8<kWide>(a.q + r * a.q_stride, at, a.cols, make_uint2(0u, 0u));
+            if (at < a.cols && at % kBlock == 0) a.scales[r * a.scale_row + (int64_t)(at / kBlock) * a.scale_block] = 0;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ tiles
+// 128 x 128 tiles, 256 threads: thread (ty, tx) holds rows ty + 16 i (i < 8) of
+// columns 8 tx .. 8 tx + 7, 8 loads in flight; a warp covers two rows of 128
+// columns.  Column blocks (one scale a column) and square blocks (one a tile)
+// differ in how far the maximum is reduced.
+struct TileArgs {
+    int64_t x_stride, x_group;      // elements
+    uint8_t *q;
+    int64_t q_stride, q_group;
+    uint8_t *scales;
+    int64_t scale_stride;           // columns: bytes between 128-row blocks
+    const int *ends;                // columns: group ends
+    int64_t rows, tiles;            // rows of x (of each group); tiles in all
+    int32_t G, cols, row_tiles, col_tiles;
+    bool e5m2;
+};
+
+template <typename T, bool kWide, bool kSquare>
+__global__ void __launch_bounds__(kQThreads)
+quantize_tiles_kernel(const T *__restrict__ x, TileArgs a) {
+    __shared__ uint32_t top[16][128];
+    __shared__ uint32_t bytes[128];
+    __shared__ GroupTable table;
+    grid_dependency_wait();
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, lane = tid & 31, w = tid >> 5;
+    const int fexp = a.e5m2 ? 15 : 8;
+    if (!kSquare) {
+        if (w == 0) build_group_table<true>(a.ends, a.G, (int)a.rows, 1, table);
+        __syncthreads();
+    }
+    for (int64_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
+        const int64_t rb = tile / a.col_tiles;
+        const int c0 = (int)(tile - rb * a.col_tiles) * 128, c = c0 + tx * 8;
+        const T *src = x;
+        uint8_t *dst = a.q;
+        int64_t valid, dst_rows = 128;   // rows of the tile that hold data, and that exist in q
+        int64_t scale_at;
+        if (kSquare) {
+            const int64_t g = rb / a.row_tiles, r0 = (rb - g * a.row_tiles) * 128;
+            src += g * a.x_group + r0 * a.x_stride;
+            dst += g * a.q_group + r0 * a.q_stride;
+            valid = dst_rows = min((int64_t)128, a.rows - r0);
+            scale_at = rb * a.col_tiles + c0 / 128;
+        } else {
+            valid = 0;
+            const int64_t p = rb * 128;
+            if (p < table.pstart[kMaxGroups]) {
+                const int g = find_group_pstart(table, kMaxGroups, (int)p);
+                const int64_t r0 = p - table.pstart[g];
+                valid = min((int64_t)128, table.size[g] - r0);
+                src += (table.begin[g] + r0) * a.x_stride;
+            }
+            dst += p * a.q_stride;
+            scale_at = rb * a.scale_stride + c0;
+        }
+        Pack<T, 8> v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = ty + 16 * i;
+            if (r < valid) v[i] = load8<T, kWide>(src + r * a.x_stride, c, a.cols);
+            else memset(&v[i], 0, sizeof(v[i]));
+        }
+        uint32_t m[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) m[u] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int u = 0; u < 8; ++u) m[u] = max(m[u], magnitude(to_f32(v[i].v[u])));
+        if (kSquare) {
+            uint32_t all = 0;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) all = max(all, m[u]);
+            all = __reduce_max_sync(0xffffffffu, all);
+            if (lane == 0) top[0][w] = all;
+            __syncthreads();
+            all = top[0][0];
+#pragma unroll
+            for (int u = 1; u < kQThreads / 32; ++u) all = max(all, top[0][u]);
+            const uint32_t byte = scale_byte(all, fexp);
+            if (tid == 0) a.scales[scale_at] = (uint8_t)byte;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) m[u] = byte;
+        } else {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) top[ty][tx * 8 + u] = m[u];
+            __syncthreads();
+            if (tid < 128) {
+                uint32_t all = 0;
+#pragma unroll
+                for (int u = 0; u < 16; ++u) all = max(all, top[u][tid]);
+                const uint32_t byte = scale_byte(all, fexp);
+                bytes[tid] = byte;
+                if (c0 + tid < a.cols) a.scales[scale_at + tid] = (uint8_t)byte;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < 8; ++u) m[u] = bytes[tx * 8 + u];
+        }
+        uint32_t nan[2] = {0u, 0u};   // bytes of the columns whose block holds no finite scale
+        float s[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if (m[u] == 255u) nan[u >> 2] |= 0xffu << (8 * (u & 3));
+            s[u] = inverse_scale(min(m[u], 254u));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = ty + 16 * i;
+            float f[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) f[u] = to_f32(v[i].v[u]) * s[u];
+            uint2 q;
+            q.x = two_eight_bit(f[0], f[1], a.e5m2) | two_eight_bit(f[2], f[3], a.e5m2) << 16;
+            q.y = two_eight_bit(f[4], f[5], a.e5m2) | two_eight_bit(f[6], f[7], a.e5m2) << 16;
+            if (r < valid) {
+                q.x = (q.x & ~nan[0]) | (0x7f7f7f7fu & nan[0]);
+                q.y = (q.y & ~nan[1]) | (0x7f7f7f7fu & nan[1]);
+            }
+            if (r < dst_rows) store8<kWide>(dst + r * a.q_stride, c, a.cols, q);
+        }
+        __syncthreads();
+    }
+}
+
+// ------------------------------------------------------------------ host side
+int in_bytes(mx_dtype t) { return t == MX_F32 ? 4 : t == MX_BF16 || t == MX_F16 ? 2 : 0; }
+
+bool wide_ok(const void *x, int64_t x_stride, int64_t x_group, int es, const void *q, int64_t q_stride, int64_t q_group,
+             int64_t cols) {
+    return cols % 8 == 0 && aligned_to(x, 16) && (x_stride * es) % 16 == 0 && (x_group * es) % 16 == 0 && aligned_to(q, 8) &&
+           q_stride % 8 == 0 && q_group % 8 == 0;
+}
+
+template <typename T, bool kWide>
+mx_status rows_typed(const void *x, int64_t x_stride, const RowsArgs &a, int block, int64_t grid, cudaStream_t stream) {
+    const T *p = static_cast<const T *>(x);
+    const bool order = a.row_of_slot != nullptr;
+    if (block == 128)
+        return order ? launch(quantize_rows_kernel<T, kWide, 128, true>, grid, kQThreads, 0, stream, p, x_stride, a)
+                     : launch(quantize_rows_kernel<T, kWide, 128, false>, grid, kQThreads, 0, stream, p, x_stride, a);
+    return order ? launch(quantize_rows_kernel<T, kWide, 32, true>, grid, kQThreads, 0, stream, p, x_stride, a)
+                 : launch(quantize_rows_kernel<T, kWide, 32, false>, grid, kQThreads, 0, stream, p, x_stride, a);
+}
+
+template <typename T, bool kSquare>
+mx_status tiles_typed(const void *x, const TileArgs &a, bool wide, cudaStream_t stream) {
+    int sms = 0;
+    if (mx_status st = mx_device_sms(&sms); st != MX_OK) return st;
+    const int64_t cap = (int64_t)sms * 4;
+    const int64_t grid = a.tiles < cap ? a.tiles : cap;
+    const T *p = static_cast<const T *>(x);
+    return wide ? launch(quantize_tiles_kernel<T, true, kSquare>, grid, kQThreads, 0, stream, p, a)
+                : launch(quantize_tiles_kernel<T, false, kSquare>, grid, kQThreads, 0, stream, p, a);
+}
+
+template <bool kSquare>
+mx_status tiles_any(const void *x, mx_dtype dtype, const TileArgs &a, bool wide, cudaStream_t stream) {
+    if (dtype == MX_F32) return tiles_typed<float, kSquare>(x, a, wide, stream);
+    if (dtype == MX_BF16) return tiles_typed<__nv_bfloat16, kSquare>(x, a, wide, stream);
+    return tiles_typed<__half, kSquare>(x, a, wide, stream);
+}
+
+bool eight_bit_type(mx_dtype t) { return t == MX_E4M3 || t == MX_E5M2; }
+
+}  // namespace
+}  // namespace mx
+
+extern "C" {
+
+mx_status mx_quantize_rows(const void *x, mx_dtype dtype, int64_t rows, int64_t cols, int64_t x_stride, int32_t block,
+                           mx_dtype out_dtype, const int32_t *row_of_slot, int32_t choices, const int32_t *group_ends,
+                           int32_t num_experts, uint8_t *q, int64_t q_stride, uint8_t *scales, int64_t scale_row_stride,
+                           int64_t scale_block_stride, cudaStream_t stream) {
+    const int es = mx::in_bytes(dtype);
+    if (es == 0 || !mx::eight_bit_type(out_dtype) || (block != 128 && block != 32)) return MX_ERR_INVALID_ARG;
+    if (rows < 0 || cols < 0 || rows > mx::kOpsMaxExtent || cols > mx::kOpsMaxExtent) return MX_ERR_INVALID_ARG;
+    if (x_stride < cols || q_stride < cols || scale_row_stride < 1 || scale_block_stride < 1) return MX_ERR_INVALID_ARG;
+    const bool order = row_of_slot != nullptr;
+    if (order && (choices < 1 || rows * choices > mx::kOpsMaxExtent || num_experts < 1 || num_experts > MX_MAX_GROUPS ||
+                  group_ends == nullptr))
+        return MX_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0) return MX_OK;
+    if (x == nullptr || q == nullptr || scales == nullptr) return MX_ERR_INVALID_ARG;
+    if (!mx::aligned_to(x, es) || !mx::aligned_to(row_of_slot, 4) || !mx::aligned_to(group_ends, 4)) return MX_ERR_MISALIGNED;
+    mx::RowsArgs a = {};
+    a.q = q;
+    a.q_stride = q_stride;
+    a.scales = scales;
+    a.scale_row = scale_row_stride;
+    a.scale_block = scale_block_stride;
+    a.row_of_slot = row_of_slot;
+    a.last_end = order ? group_ends + num_experts - 1 : nullptr;
+    a.in_rows = rows;
+    a.out_rows = order ? rows * choices : rows;
+    a.cols = (int32_t)cols;
+    a.k = choices;
+    a.segments = (int32_t)mx::div_up(cols, 256);
+    a.e5m2 = out_dtype == MX_E5M2;
+    const int64_t grid = mx::div_up(rows, 32) * a.segments;
+    if (grid > INT_MAX) return MX_ERR_UNSUPPORTED;
+    int sms = 0;
+    if (mx_status st = mx_device_sms(&sms); st != MX_OK) return st;
+    const bool wide = mx::wide_ok(x, x_stride, 0, es, q, q_stride, 0, cols);
+#define MX_ROWS(T) (wide ? mx::rows_typed<T, true>(x, x_stride, a, block, grid, stream) : mx::rows_typed<T, false>(x, x_stride, a, block, grid, stream))
+    if (dtype == MX_F32) return MX_ROWS(float);
+    if (dtype == MX_BF16) return MX_ROWS(__nv_bfloat16);
+    return MX_ROWS(__half);
+#undef MX_ROWS
+}
+
+int64_t mx_padded_rows(int64_t rows, int32_t num_groups) {
+    if (rows < 0 || rows > mx::kOpsMaxExtent || num_groups < 1 || num_groups > MX_MAX_GROUPS) return 0;
+    return mx::up_to(rows, 128) + 128ll * num_groups;
+}
+
+mx_status mx_quantize_cols(const void *x, mx_dtype dtype, int64_t rows, int64_t cols, int64_t x_stride,
+                           const int32_t *group_ends, int32_t num_groups, mx_dtype out_dtype, uint8_t *q, int64_t q_stride,
+                           uint8_t *scales, int64_t scale_stride, cudaStream_t stream) {
+    const int es = mx::in_bytes(dtype);
+    if (es == 0 || !mx::eight_bit_type(out_dtype) || num_groups < 1 || num_groups > MX_MAX_GROUPS) return MX_ERR_INVALID_ARG;
+    if (rows < 0 || cols < 0 || rows > mx::kOpsMaxExtent || cols > mx::kOpsMaxExtent) return MX_ERR_INVALID_ARG;
+    if (x_stride < cols || q_stride < cols || scale_stride < cols) return MX_ERR_INVALID_ARG;
+    if (cols == 0) return MX_OK;
+    if ((rows > 0 && x == nullptr) || q == nullptr || scales == nullptr || group_ends == nullptr) return MX_ERR_INVALID_ARG;
+    if (!mx::aligned_to(x, es) || !mx::aligned_to(group_ends, 4)) return MX_ERR_MISALIGNED;
+    mx::TileArgs a = {};
+    a.x_stride = x_stride;
+    a.q = q;
+    a.q_stride = q_stride;
+    a.scales = scales;
+    a.scale_stride = scale_stride;
+    a.ends = group_ends;
+    a.rows = rows;
+    a.G = num_groups;
+    a.cols = (int32_t)cols;
+    a.col_tiles = (int32_t)mx::div_up(cols, 128);
+    a.tiles = mx_padded_rows(rows, num_groups) / 128 * a.col_tiles;
+    a.e5m2 = out_dtype == MX_E5M2;
+    return mx::tiles_any<false>(x, dtype, a, mx::wide_ok(x, x_stride, 0, es, q, q_stride, 0, cols), stream);
+}
+
+mx_status mx_quantize_blocks(const void *x, mx_dtype dtype, int64_t groups, int64_t rows, int64_t cols, int64_t x_group_stride,
+                             int64_t x_stride, mx_dtype out_dtype, uint8_t *q, int64_t q_group_stride, int64_t q_stride,
+                             uint8_t *scales, cudaStream_t stream) {
+    const int es = mx::in_bytes(dtype);
+    if (es == 0 || !mx::eight_bit_type(out_dtype)) return MX_ERR_INVALID_ARG;
+    if (groups < 0 || rows < 0 || cols < 0 || groups > mx::kOpsMaxExtent || rows > mx::kOpsMaxExtent || cols > mx::kOpsMaxExtent)
+        return MX_ERR_INVALID_ARG;
+    if (x_stride < cols || q_stride < cols || x_group_stride < 0 || q_group_stride < 0) return MX_ERR_INVALID_ARG;
+    if (groups == 0 || rows == 0 || cols == 0) return MX_OK;
+    if (x == nullptr || q == nullptr || scales == nullptr) return MX_ERR_INVALID_ARG;
+    if (groups > 1 && q_group_stride < (rows - 1) * q_stride + cols) return MX_ERR_INVALID_ARG;
+    if (!mx::aligned_to(x, es)) return MX_ERR_MISALIGNED;
+    mx::TileArgs a = {};
+    a.x_stride = x_stride;
+    a.x_group = groups > 1 ? x_group_stride : 0;
+    a.q = q;
+    a.q_stride = q_stride;
+    a.q_group = groups > 1 ? q_group_stride : 0;
+    a.scales = scales;
+    a.rows = rows;
+    a.cols = (int32_t)cols;
+    a.row_tiles = (int32_t)mx::div_up(rows, 128);
+    a.col_tiles = (int32_t)mx::div_up(cols, 128);
+    if (mx::div_up(rows, 128) * a.col_tiles > INT64_MAX / mx::kOpsMaxExtent) return MX_ERR_UNSUPPORTED;
+    a.tiles = groups * a.row_tiles * a.col_tiles;
+    a.e5m2 = out_dtype == MX_E5M2;
+    return mx::tiles_any<true>(x, dtype, a, mx::wide_ok(x, x_stride, a.x_group, es, q, q_stride, a.q_group, cols), stream);
+}
+
+}  // extern "C"

@@ -931,6 +931,33 @@ mx_status run(mx_group_dim dim, const uint8_t *scales, int64_t rows, int64_t col
 // Shared with mx_inverse.cu (C++ linkage, not part of the C ABI).
 mx_status mx_record_cuda_error(cudaError_t e) { return mx::cuda_status(e); }
 cudaError_t mx_inverse_flags(unsigned int *flags, int clear);   // defined in mx_inverse.cu
+cudaError_t mx_matmul_flags(unsigned int *flags, int clear);    // defined in mx_matmul.cu
+
+// The SM count of the current device, whose context is current in this thread afterwards.
+mx_status mx_device_sms(int *sms) {
+    const mx::DeviceInfo *d = nullptr;
+    if (mx_status st = mx::device_info(&d); st != MX_OK) return st;
+    *sms = d->sms;
+    return MX_OK;
+}
+
+// A tensor map over bytes of `rank` 2 or 3 with the 128-byte swizzle, for the
+// current device; strides[i] is that of dimension i + 1, boxes are 128 bytes wide.
+mx_status mx_encode_bytes_map(CUtensorMap *map, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
+                              const uint32_t *box) {
+    const mx::DeviceInfo *d = nullptr;
+    if (mx_status st = mx::device_info(&d); st != MX_OK) return st;
+    auto encode = mx::encode_fn();
+    if (encode == nullptr) return mx::cuda_status(cudaErrorSymbolNotFound);
+    const cuuint32_t estride[3] = {1, 1, 1};
+    cuuint64_t gdim[3], gstride[2];
+    for (int i = 0; i < rank; ++i) gdim[i] = dims[i];
+    for (int i = 0; i + 1 < rank; ++i) gstride[i] = strides[i];
+    CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void *>(base), gdim, gstride, box, estride,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? MX_OK : mx::cuda_status(static_cast<cudaError_t>(r));   // driver code
+}
 
 // A 2-D uint8 tensor map over `rows` rows of `width` bytes at `row_stride`
 // (a multiple of 16) from the 16-byte aligned `base`, boxes of box_w x box_h
@@ -1005,7 +1032,9 @@ mx_status mx_device_flags(uint32_t *flags, int clear) {
     if (cudaError_t e = cudaMemcpyFromSymbol(&v, mx::g_mx_flags, sizeof(v)); e != cudaSuccess)
         return mx::cuda_status(e);
     if (cudaError_t e = mx_inverse_flags(&inv, clear); e != cudaSuccess) return mx::cuda_status(e);
-    *flags = v | inv;
+    unsigned int mat = 0;
+    if (cudaError_t e = mx_matmul_flags(&mat, clear); e != cudaSuccess) return mx::cuda_status(e);
+    *flags = v | inv | mat;
     if (clear) {
         const unsigned int zero = 0;
         if (cudaError_t e = cudaMemcpyToSymbol(mx::g_mx_flags, &zero, sizeof(zero)); e != cudaSuccess)
