@@ -99,7 +99,7 @@ PRODUCT_K = dict(a=0x1000, a_dtype=B.MX_E4M3, a_stride=64, a_scales=0x2000, a_sc
     ("mx_grouped_matmul_m", PRODUCT, dict(b_group_stride=2056), MISALIGNED),
     ("mx_grouped_matmul_m", PRODUCT, dict(out=0x8001), MISALIGNED),
     ("mx_grouped_matmul_m", PRODUCT, dict(block=32, a_scales=0x2004), MISALIGNED),
-    ("mx_grouped_matmul_m", PRODUCT, dict(block=32, b_layout=B.MX_B_KN), UNSUPPORTED),
+    ("mx_grouped_matmul_m", PRODUCT, dict(block=32, b_layout=B.MX_B_KN, b_group_stride=4096), UNSUPPORTED),
     ("mx_grouped_matmul_m", PRODUCT, dict(rows=0), OK),
     ("mx_grouped_matmul_k", PRODUCT_K, dict(padded_rows=200), INVALID),
     ("mx_grouped_matmul_k", PRODUCT_K, dict(padded_rows=0), INVALID),
