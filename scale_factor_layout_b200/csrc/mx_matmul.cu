@@ -14,13 +14,19 @@
 // writes such a tile with each byte four times, so both kinds run the same
 // loop, and the scales cost no arithmetic outside the tensor cores.
 //
-// A CTA per SM walks output tiles of 128 x kN.  Its warps: 0 loads operands by
-// TMA into a ring of stages of 128 along the contraction; 1 issues the matrix
-// instructions; 2 brings the scales; 3 holds the tensor memory; 4..7 empty the
-// accumulators into the output.  Operands whose contraction is the outer
-// dimension in memory (weights read for the input gradient, both operands of
-// the weight gradient) are loaded as they are and read through descriptors of
-// that order: nothing is transposed in memory.
+// A CTA, or a pair of CTAs of a cluster, per SM (or two) walks output tiles of
+// kTileRows x kN.  The warps of a CTA: 0 loads operands by TMA into a ring of
+// stages of 128 along the contraction; 1 issues the matrix instructions (in a
+// pair, that of rank 0 for both); 2 and 3 bring the scales, each for every
+// other stage; 4..11 empty the accumulators into the output, two warps for
+// each quarter of the rows.  A pair works on 256 rows x 256 columns: each CTA
+// holds 128 rows of a and half of b's 256, so a stage brings 32 KB for the work
+// that takes 48 KB alone.  Shared memory bounds the loop (a stage is written
+// once and read once, 128 bytes a clock), so that is what a pair wins.
+// Operands whose contraction is the outer dimension in memory (weights read
+// for the input gradient, both operands of the weight gradient) are loaded as
+// they are and read through descriptors of that order: nothing is transposed
+// in memory.
 
 #include <climits>
 #include <mutex>
@@ -28,9 +34,9 @@
 #include "mx_ops.cuh"
 #include "mx_tcgen05.cuh"
 
-// A tensor map over bytes, with the 128-byte swizzle (defined in mx_rearrange.cu).
-mx_status mx_encode_bytes_map(CUtensorMap *map, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
-                              const uint32_t *box);
+// A tensor map over bytes with a swizzle, or over 32-bit words without (defined in mx_rearrange.cu).
+mx_status mx_encode_map(CUtensorMap *map, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
+                        const uint32_t *box, CUtensorMapSwizzle swizzle);
 
 namespace mx {
 namespace {
@@ -40,12 +46,14 @@ __device__ unsigned int g_matmul_flags = 0;
 enum Form { kFormNK = 0, kFormKN = 1, kFormOuter = 2 };
 enum ScaleForm { kScales128 = 0, kScales32 = 1 };
 
-constexpr int kTileM = 128;
 constexpr int kTileK = 128;
-constexpr int kMatThreads = 256;
-constexpr int kOperandBytes = kTileM * kTileK;   // a 128 x 128 panel of either operand
+constexpr int kMatThreads = 384;
+constexpr int kDrainWarps = 8;
+constexpr int kOutRow = 64, kOutBytes = 32 * kOutRow;   // bytes of a row, and of a warp's rows, in a store
+constexpr int kPanelBytes = 128 * kTileK;   // 128 rows (or columns) of an operand in a stage
 constexpr int kTmemColumns = 512;
-constexpr int kScaleColumn = 480;                // 2 sets of 4 + 8 columns of scales
+constexpr int kScaleColumn = 480;           // 2 sets of 4 + 8 columns of scales
+constexpr int kStrip = 8;                   // tiles of a strip of columns
 
 struct MatArgs {
     const int *ends;
@@ -55,58 +63,91 @@ struct MatArgs {
     void *out;
     int64_t out_stride, out_group;          // elements
     int32_t G, rows;                        // rows: of a (row groups), of both operands (contraction groups)
-    int32_t M, N, K;                        // M: contraction groups only
+    int32_t M, N;                           // M: contraction groups only
     int32_t n_tiles, m_tiles, k_tiles;      // m_tiles: contraction groups only
     int32_t out_type;                       // 0 f32, 1 bf16, 2 f16
     uint32_t idesc;
-    bool wide_out;
+    int32_t n_first;                        // row groups: tiles of columns that go first, see tile_at
+    bool tma_out;                           // out's rows start on 16-byte boundaries
 };
 
-template <int kN>
+struct Maps { CUtensorMap a, b, sa, sb, out; };   // sa, sb: scales of 32 only
+
+template <int kScales, int kN, bool kPair>
 struct Shared {
-    static constexpr int kStages = kN == 256 ? 4 : 6;
-    static constexpr int kPanels = kN / 128;
-    static constexpr int kAccs = kN == 256 ? 1 : 2;
-    static constexpr int kStageBytes = (1 + kPanels) * kOperandBytes;
+    static constexpr int kTileRows = kPair ? 256 : 128;
+    static constexpr int kPanels = kN / 128;                  // 128-column panels of the tile
+    static constexpr int kPanelsHere = kPair ? 1 : kPanels;   // of them in this CTA
+    static constexpr int kStages = 192 / (16 + 16 * kPanelsHere);
+    static constexpr int kStageBytes = (1 + kPanelsHere) * kPanelBytes;
     static constexpr int kScaleBytes = (1 + kPanels) * 512;
+    // scales of 128: a slot holds those of four stages; of 32: of one, and comes with its operands
+    static constexpr int kScaleSlots = kScales == kScales128 ? 4 : kStages;
     alignas(1024) uint8_t operands[kStages][kStageBytes];
-    alignas(128) uint8_t scales[kStages][kScaleBytes];
+    alignas(1024) uint8_t out[kDrainWarps][kOutBytes];
+    alignas(128) uint8_t scales[kScaleSlots][kScaleBytes];
     GroupTable table;
-    alignas(8) uint64_t full[kStages], empty[kStages], acc_full[kAccs], acc_empty[kAccs], drain;
+    alignas(8) uint64_t full[kStages], empty[kStages], scale_full[kScaleSlots], scale_empty[kScaleSlots];
+    alignas(8) uint64_t acc_full, acc_empty, drain;
     uint32_t tmem;
     volatile int abort;
 };
 
 struct Tile {
-    int32_t g, row0, rows, n0, k_tiles;   // row0: first row of a (row groups) or column of a (contraction groups)
+    int32_t g, row0, rows, n0, n, k_tiles;   // n: columns of the tile, a multiple of 32; row0: this CTA's first row of a (row groups) or column of a (contraction groups)
     int32_t k_base;                       // contraction groups: first row of the operands
-    int32_t scale_row;                    // blocked scales: the 128-row tile of a's scales
+    int32_t scale_row;                    // scales of 32: the 128-row tile of a's scales
 };
 
-template <int kForm, int kN>
-__device__ __forceinline__ Tile tile_at(const GroupTable &table, const MatArgs &a, int t) {
+// Tiles of a group go in strips of kStrip tiles of columns, row by row within
+// a strip, so that the tiles in flight share both operands in L2.  CTAs take
+// tiles in turn; where the last column of tiles is narrow (n_first of n_tiles
+// go first), those of all groups go last, which evens the CTAs' shares out.
+template <int kForm, int kN, int kTileRows>
+__device__ __forceinline__ Tile tile_at(const GroupTable &table, const MatArgs &a, int t, int rank) {
     Tile o;
+    int mt, nt;
+    if (kForm != kFormOuter && t >= table.istart[kMaxGroups] * a.n_first) {
+        t -= table.istart[kMaxGroups] * a.n_first;
+        o.g = find_group(table, kMaxGroups, t);
+        mt = t - table.istart[o.g];
+        nt = a.n_first;
+    } else {
+        int local, m_tiles, n_tiles;
+        if (kForm == kFormOuter) {
+            m_tiles = a.m_tiles;
+            n_tiles = a.n_tiles;
+            o.g = t / (m_tiles * n_tiles);
+            local = t - o.g * (m_tiles * n_tiles);
+        } else {
+            n_tiles = a.n_first;
+            o.g = find_group(table, kMaxGroups, t / n_tiles);
+            local = t - table.istart[o.g] * n_tiles;
+            m_tiles = table.istart[o.g + 1] - table.istart[o.g];
+        }
+        const int strip = local / (m_tiles * kStrip);
+        local -= strip * m_tiles * kStrip;
+        const int width = min(kStrip, n_tiles - strip * kStrip);
+        mt = local / width;
+        nt = strip * kStrip + local - mt * width;
+    }
+    const int row = mt * kTileRows + rank * 128;
+    o.n0 = nt * kN;
+    o.n = min(kN, (a.N - o.n0 + 31) & ~31);
     if (kForm == kFormOuter) {
-        const int per = a.m_tiles * a.n_tiles;
-        o.g = t / per;
-        const int local = t - o.g * per, mt = local / a.n_tiles;
-        o.row0 = mt * kTileM;
-        o.rows = min(kTileM, a.M - o.row0);
-        o.n0 = (local - mt * a.n_tiles) * kN;
+        o.row0 = row;
+        o.rows = min(128, a.M - row);
         o.k_base = table.pstart[o.g];
         o.k_tiles = (table.size[o.g] + kTileK - 1) / kTileK;
         o.scale_row = 0;
     } else {
-        o.g = find_group(table, kMaxGroups, t);
-        const int local = t - table.istart[o.g], mt = local / a.n_tiles;
-        o.row0 = table.begin[o.g] + mt * kTileM;
-        o.rows = min(kTileM, table.size[o.g] - mt * kTileM);
-        o.n0 = (local - mt * a.n_tiles) * kN;
+        o.row0 = table.begin[o.g] + row;
+        o.rows = min(128, table.size[o.g] - row);
         o.k_base = 0;
         o.k_tiles = a.k_tiles;
-        o.scale_row = table.pstart[o.g] / kTileM + mt;
+        o.scale_row = (table.pstart[o.g] + row) / 128;
     }
-    return o;
+    return o;   // rows may be 0 or less in the second CTA of a pair
 }
 
 // A bounded wait that also ends when another warp of the CTA has given up.
@@ -125,303 +166,408 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, vo
     }
 }
 
-// Scale bytes of four rows (lane, lane + 32, ...) for four steps of the
-// contraction, one word a step.
-struct RowScales { uint32_t step[4]; };
-__device__ __forceinline__ RowScales load_row_scales(const uint8_t *s, int64_t row_stride, int64_t block_stride, int row0,
-                                                     int rows, int block0, int blocks, int lane) {
-    RowScales o;
+// Scale bytes of rows lane + 32 i of a panel for four steps of the contraction:
+// a line of the 128 x 4 tile.  Rows past the last are read as the last one,
+// since what they scale is not stored; so are steps.
+struct LineSource {
+    const uint8_t *p[4];
+    __device__ __forceinline__ LineSource() {}
+    __device__ __forceinline__ LineSource(const uint8_t *s, int64_t stride, int row0, int rows, int lane) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        o.step[k] = 0;
+        for (int i = 0; i < 4; ++i) p[i] = s + (int64_t)max(0, min(row0 + lane + 32 * i, rows - 1)) * stride;
+    }
+    __device__ __forceinline__ void load(uint32_t (&b)[16], int k, int last, int64_t stride) const {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = row0 + lane + 32 * i;
-            uint32_t b = 127;
-            if (r < rows && block0 + k < blocks) b = s[r * row_stride + (block0 + k) * block_stride];
-            o.step[k] |= b << (8 * i);
+        for (int u = 0; u < 4; ++u) {
+            const int64_t at = (int64_t)min(k + u, last) * stride;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[4 * i + u] = __ldg(p[i] + at);
         }
     }
-    return o;
+};
+__device__ __forceinline__ uint32_t four_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return a | b << 8 | c << 16 | d << 24;
 }
-// A line of the tile: rows lane + 32 i, each byte for all four groups of 32.
-__device__ __forceinline__ uint4 scale_line(uint32_t rows4) {
-    return make_uint4(__byte_perm(rows4, 0, 0x0000), __byte_perm(rows4, 0, 0x1111), __byte_perm(rows4, 0, 0x2222),
-                      __byte_perm(rows4, 0, 0x3333));
+__device__ __forceinline__ uint4 tile_line(const uint32_t (&b)[16]) {
+    return make_uint4(four_bytes(b[0], b[1], b[2], b[3]), four_bytes(b[4], b[5], b[6], b[7]),
+                      four_bytes(b[8], b[9], b[10], b[11]), four_bytes(b[12], b[13], b[14], b[15]));
 }
 
 template <typename T>
-__device__ __forceinline__ void store_row(T *dst, const uint32_t (&v)[32], int valid, bool wide) {
-    if (wide && valid >= 32) {
-        constexpr int N = 16 / sizeof(T);
+__device__ __forceinline__ void store_row(void *out, int64_t at, const uint32_t (&v)[32], int valid) {
+    T *dst = static_cast<T *>(out) + at;
 #pragma unroll
-        for (int i = 0; i < 32; i += N) {
-            Pack<T, N> p;
+    for (int i = 0; i < 32; ++i)
+        if (i < valid) dst[i] = from_f32<T>(__uint_as_float(v[i]));
+}
+
+// 64 bytes of this lane's row into the warp's box of 32 rows, with the 64-byte
+// swizzle: 16-byte piece c of row r sits at piece c ^ (r / 2 % 4).
+template <typename T>
+__device__ __forceinline__ void stage_row(uint8_t *box, const uint32_t *v, int lane) {
+    constexpr int N = 16 / sizeof(T);
 #pragma unroll
-            for (int u = 0; u < N; ++u) p.v[u] = from_f32<T>(__uint_as_float(v[i + u]));
-            *reinterpret_cast<Pack<T, N> *>(dst + i) = p;
-        }
-    } else {
+    for (int c = 0; c < 4; ++c) {
+        Pack<T, N> p;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < valid) dst[i] = from_f32<T>(__uint_as_float(v[i]));
+        for (int u = 0; u < N; ++u) p.v[u] = from_f32<T>(__uint_as_float(v[c * N + u]));
+        *reinterpret_cast<Pack<T, N> *>(box + lane * kOutRow + ((c ^ (lane >> 1 & 3)) << 4)) = p;
     }
 }
 
-template <int kForm, int kScales, int kN>
+template <int kForm, int kScales, int kN, bool kPair>
 __global__ void __launch_bounds__(kMatThreads, 1)
-grouped_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const MatArgs a) {
-    using Sh = Shared<kN>;
-    constexpr int kStages = Sh::kStages, kPanels = Sh::kPanels, kAccs = Sh::kAccs;
+grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
+    using Sh = Shared<kScales, kN, kPair>;
+    constexpr int kScaleSlots = Sh::kScaleSlots;
+    constexpr int kStages = Sh::kStages, kPanels = Sh::kPanels, kPanelsHere = Sh::kPanelsHere, kTileRows = Sh::kTileRows;
     constexpr bool kOuterA = kForm == kFormOuter, kOuterB = kForm != kFormNK;
+    constexpr int kCtas = kPair ? 2 : 1;
+    constexpr int kScaleSteps = kScales == kScales128 ? 4 : 1;   // stages whose scales are in one slot
     extern __shared__ uint8_t dyn_smem[];
     Sh &sh = *reinterpret_cast<Sh *>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    const int rank = kPair ? (int)cluster_rank() : 0;
+    const int first = blockIdx.x / kCtas, step = gridDim.x / kCtas;
 
     if (w == 0 && lane == 0) {
-        tma_prefetch_desc(&map_a);
-        tma_prefetch_desc(&map_b);
+        tma_prefetch_desc(&maps.a);
+        tma_prefetch_desc(&maps.b);
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&sh.full[i], 2);    // operands, scales
+            mbar_init(&sh.full[i], kCtas);
             mbar_init(&sh.empty[i], 1);
         }
-        for (int i = 0; i < kAccs; ++i) {
-            mbar_init(&sh.acc_full[i], 1);
-            mbar_init(&sh.acc_empty[i], 4);   // the four warps that empty it
+        for (int i = 0; i < kScaleSlots; ++i) {
+            mbar_init(&sh.scale_full[i], kCtas);
+            mbar_init(&sh.scale_empty[i], 1);
         }
+        mbar_init(&sh.acc_full, 1);
+        mbar_init(&sh.acc_empty, kDrainWarps * kCtas);
         mbar_init(&sh.drain, 1);
         sh.abort = 0;
         fence_mbar_init();
     }
+    __syncwarp();
     grid_dependency_wait();
-    if (w == 3) tmem_alloc(&sh.tmem, kTmemColumns);
-    if (w == 2) build_group_table<true>(a.ends, a.G, a.rows, a.n_tiles, sh.table);
+    if (w == 3) tmem_alloc<kPair>(&sh.tmem, kTmemColumns);
+    if (w == 2) build_group_table<true, kTileRows>(a.ends, a.G, a.rows, 1, sh.table);
     tc_fence_before();
     __syncthreads();
+    if (kPair) cluster_sync();   // the barriers are there before the other CTA arrives on them
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    const int total = kForm == kFormOuter ? a.G * a.m_tiles * a.n_tiles : sh.table.istart[kMaxGroups];
+    const int total = kForm == kFormOuter ? a.G * a.m_tiles * a.n_tiles : sh.table.istart[kMaxGroups] * a.n_tiles;
 
     if (w == 0) {
-        if (lane == 0) {
-            uint32_t it = 0;
-            bool ok = true;
-            for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-                const Tile o = tile_at<kForm, kN>(sh.table, a, t);
-                for (int k = 0; k < o.k_tiles; ++k, ++it) {
-                    const uint32_t s = it % kStages, phase = it / kStages & 1;
-                    if (!(ok = wait_or_abort(&sh.empty[s], phase ^ 1, &sh.abort))) break;
-                    uint8_t *pa = sh.operands[s], *pb = pa + kOperandBytes;
-                    mbar_arrive_expect_tx(&sh.full[s], Sh::kStageBytes);
-                    if (kOuterA) tma_load_2d(pa, &map_a, o.row0, o.k_base + k * kTileK, &sh.full[s]);
-                    else tma_load_2d(pa, &map_a, k * kTileK, o.row0, &sh.full[s]);
-                    if (kForm == kFormNK) {
-                        tma_load_3d(pb, &map_b, k * kTileK, o.n0, o.g, &sh.full[s]);
-                    } else {
-#pragma unroll
-                        for (int p = 0; p < kPanels; ++p) {
-                            if (kForm == kFormKN)
-                                tma_load_3d(pb + p * kOperandBytes, &map_b, o.n0 + 128 * p, k * kTileK, o.g, &sh.full[s]);
-                            else
-                                tma_load_2d(pb + p * kOperandBytes, &map_b, o.n0 + 128 * p, o.k_base + k * kTileK, &sh.full[s]);
-                        }
-                    }
-                }
-            }
-            if (!ok)   // copies in flight land before the CTA leaves
-                for (uint32_t i = it < (uint32_t)kStages ? 0 : it - kStages; i < it; ++i)
-                    mbar_wait_bounded(&sh.full[i % kStages], i / kStages & 1, 1ll << 24);
-        }
-    } else if (w == 1) {
-        if (lane == 0) {
-            uint32_t it = 0, n = 0;
-            bool ok = true;
-            for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-                const Tile o = tile_at<kForm, kN>(sh.table, a, t);
-                if (o.k_tiles == 0) continue;
-                const uint32_t acc = n % kAccs;
-                if (!(ok = wait_or_abort(&sh.acc_empty[acc], (n / kAccs & 1) ^ 1, &sh.abort))) break;
-                tc_fence_after();
-                const uint32_t d = tmem + acc * kN;
-                for (int k = 0; k < o.k_tiles; ++k, ++it) {
-                    const uint32_t s = it % kStages;
-                    if (!(ok = wait_or_abort(&sh.full[s], it / kStages & 1, &sh.abort))) break;
-                    tc_fence_after();
-                    const uint32_t pa = smem_addr(sh.operands[s]), pb = pa + kOperandBytes, ps = smem_addr(sh.scales[s]);
-                    const uint32_t ta = tmem + kScaleColumn + (it & 1) * 16, tb = ta + 4;
-                    tc_copy_scales(ta, smem_desc(ps, 128, 128, 0));
-#pragma unroll
-                    for (int p = 0; p < kPanels; ++p) tc_copy_scales(tb + 4 * p, smem_desc(ps + 512 * (1 + p), 128, 128, 0));
-                    // contraction inner: 8 rows x 128 bytes apart by 1024, a step of 32 is 32 bytes;
-                    // contraction outer: panels of 128 columns, a step of 32 is 32 rows of 128 bytes
-                    const uint64_t da = kOuterA ? smem_desc(pa, kOperandBytes, 1024, 2) : smem_desc(pa, 16, 1024, 2);
-                    const uint64_t db = kOuterB ? smem_desc(pb, kOperandBytes, 1024, 2) : smem_desc(pb, 16, 1024, 2);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        tc_mma_scaled(d, da + q * (kOuterA ? 256 : 2), db + q * (kOuterB ? 256 : 2),
-                                      with_scale_byte(a.idesc, q), ta, tb, k > 0 || q > 0);
-                    tc_commit(&sh.empty[s]);
-                }
-                if (ok) tc_commit(&sh.acc_full[acc]);
-                ++n;
-            }
-            if (!ok) {   // matrix instructions in flight end before the tensor memory is freed
-                tc_commit(&sh.drain);
-                mbar_wait_bounded(&sh.drain, 0, 1ll << 24);
-            }
-        }
-    } else if (w == 2) {
         uint32_t it = 0;
         bool ok = true;
-        for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-            const Tile o = tile_at<kForm, kN>(sh.table, a, t);
-            if (kScales == kScales32) {
-                if (lane == 0) {
-                    const int nb = a.N < o.n0 + kN ? (a.N - o.n0 + 127) / 128 : kPanels;   // panels that exist
-                    const uint8_t *sa = a.sa + (int64_t)o.scale_row * a.k_tiles * 512;
-                    const uint8_t *sb = a.sb + ((int64_t)o.g * ((a.N + 127) / 128) + o.n0 / 128) * a.k_tiles * 512;
-                    for (int k = 0; k < o.k_tiles; ++k, ++it) {
-                        const uint32_t s = it % kStages;
-                        if (!(ok = wait_or_abort(&sh.empty[s], (it / kStages & 1) ^ 1, &sh.abort))) break;
-                        mbar_arrive_expect_tx(&sh.full[s], 512 * (1 + nb));
-                        bulk_load(sh.scales[s], sa + (int64_t)k * 512, 512, &sh.full[s]);
-                        for (int p = 0; p < nb; ++p)
-                            bulk_load(sh.scales[s] + 512 * (1 + p), sb + ((int64_t)p * a.k_tiles + k) * 512, 512, &sh.full[s]);
+        for (int t = first; ok && t < total; t += step) {
+            const Tile o = tile_at<kForm, kN, kTileRows>(sh.table, a, t, rank);
+            const int n0 = o.n0 + (kPair ? rank * (o.n / 2) : 0);
+            const int panels = (o.n + 127) / 128;   // of scales of 32
+            const int sb0 = (o.g * ((a.N + 127) / 128) + o.n0 / 128) * a.k_tiles;
+            for (int k = 0; k < o.k_tiles; ++k, ++it) {
+                const uint32_t s = it % kStages, phase = it / kStages & 1;
+                ok = __all_sync(0xffffffffu, wait_or_abort(&sh.empty[s], phase ^ 1, &sh.abort));
+                if (!ok) break;
+                if (elect_one()) {
+                    uint8_t *pa = sh.operands[s], *pb = pa + kPanelBytes;
+                    const uint32_t full = leader_addr<kPair>(&sh.full[s]);
+                    mbar_expect_at(full, Sh::kStageBytes + (kScales == kScales32 ? 512 * ((o.rows > 0) + panels) : 0));
+                    if (kScales == kScales32) {
+                        if (o.rows > 0) tma_load_2d_to<kPair>(sh.scales[s], &maps.sa, 0, o.scale_row * a.k_tiles + k, full);
+                        for (int p = 0; p < panels; ++p)
+                            tma_load_2d_to<kPair>(sh.scales[s] + 512 * (1 + p), &maps.sb, 0, sb0 + p * a.k_tiles + k, full);
                     }
-                }
-                ok = __shfl_sync(0xffffffffu, (int)ok, 0);
-            } else {
-                // four steps' bytes are loaded ahead of the four that are written
-                const int b0 = o.k_base / kTileK;
-                const int a_blocks = kForm == kFormOuter ? a.rows / kTileK : a.k_tiles;
-                const int a_rows = kForm == kFormOuter ? a.M : a.rows;
-                RowScales na, nb[kPanels];
-                auto fetch = [&](int k) {
-                    na = load_row_scales(a.sa, a.sa_row, a.sa_block, o.row0, a_rows, b0 + k, a_blocks, lane);
+                    if (kOuterA) tma_load_2d_to<kPair>(pa, &maps.a, o.row0, o.k_base + k * kTileK, full);
+                    else tma_load_2d_to<kPair>(pa, &maps.a, k * kTileK, o.row0, full);
+                    if (kForm == kFormNK) {
+                        tma_load_3d_to<kPair>(pb, &maps.b, k * kTileK, n0, o.g, full);
+                    } else {
 #pragma unroll
-                    for (int p = 0; p < kPanels; ++p) {
-                        if (kForm == kFormOuter) {
-                            nb[p] = load_row_scales(a.sb, a.sb_row, a.sb_block, o.n0 + 128 * p, a.N, b0 + k, a_blocks, lane);
-                        } else {
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                const int n = o.n0 + 128 * p;
-                                uint32_t b = 127;
-                                if (n < a.N && k + u < o.k_tiles)
-                                    b = a.sb[o.g * a.sb_group + (n / 128) * a.sb_row + (k + u) * a.sb_block];
-                                nb[p].step[u] = b * 0x01010101u;
-                            }
+                        for (int p = 0; p < kPanelsHere; ++p) {
+                            if (kForm == kFormKN)
+                                tma_load_3d_to<kPair>(pb + p * kPanelBytes, &maps.b, n0 + 128 * p, k * kTileK, o.g, full);
+                            else
+                                tma_load_2d_to<kPair>(pb + p * kPanelBytes, &maps.b, n0 + 128 * p, o.k_base + k * kTileK, full);
                         }
                     }
-                };
-                fetch(0);
-                for (int k = 0; ok && k < o.k_tiles; k += 4) {
-                    const RowScales ca = na;
-                    RowScales cb[kPanels];
-#pragma unroll
-                    for (int p = 0; p < kPanels; ++p) cb[p] = nb[p];
-                    if (k + 4 < o.k_tiles) fetch(k + 4);
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        if (!ok || k + u >= o.k_tiles) break;
-                        const uint32_t s = it % kStages;
-                        ok = wait_or_abort(&sh.empty[s], (it / kStages & 1) ^ 1, &sh.abort);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) break;
-                        *reinterpret_cast<uint4 *>(sh.scales[s] + 16 * lane) = scale_line(ca.step[u]);
-#pragma unroll
-                        for (int p = 0; p < kPanels; ++p)
-                            *reinterpret_cast<uint4 *>(sh.scales[s] + 512 * (1 + p) + 16 * lane) = scale_line(cb[p].step[u]);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sh.full[s]);
-                        ++it;
-                    }
                 }
+                __syncwarp();
             }
         }
-    } else if (w >= 4) {
-        const int quarter = w & 3;
+        if (!ok) {   // copies in flight, a few microseconds' worth, land before the CTA leaves
+            const long long t0 = clock64();
+            while (clock64() - t0 < (1ll << 22)) {}
+        }
+    } else if (w == 1) {
+        uint32_t it = 0, n = 0, sc = 0;
+        bool ok = rank == 0;
+        // contraction inner: 8 rows x 128 bytes apart by 1024, a step of 32 is 32 bytes;
+        // contraction outer: panels of 128 columns, a step of 32 is 32 rows of 128 bytes
+        const uint32_t p0 = smem_addr(sh.operands[0]), s0 = smem_addr(sh.scales[0]);
+        const uint64_t desc_a = smem_desc(p0, kOuterA ? kPanelBytes : 16, 1024, 2);
+        const uint64_t desc_b = smem_desc(p0 + kPanelBytes, kOuterB ? kPanelBytes : 16, 1024, 2);
+        const uint64_t desc_s = smem_desc(s0, 128, 128, 0);
+        for (int t = first; ok && t < total; t += step) {
+            const Tile o = tile_at<kForm, kN, kTileRows>(sh.table, a, t, 0);
+            if (o.k_tiles == 0) continue;
+            const uint32_t idesc = a.idesc | (uint32_t)(o.n / 8) << 17 | (uint32_t)(kTileRows / 16) << 24;
+            ok = __all_sync(0xffffffffu, wait_or_abort(&sh.acc_empty, (n & 1) ^ 1, &sh.abort));
+            if (!ok) break;
+            tc_fence_after();
+            for (int k = 0; k < o.k_tiles; ++k, ++it) {
+                const uint32_t s = it % kStages, slot = sc % kScaleSlots;
+                const bool scales = k % kScaleSteps == 0;   // this stage brings new ones
+                if (kScales == kScales128 && scales)
+                    ok = __all_sync(0xffffffffu, wait_or_abort(&sh.scale_full[slot], sc / kScaleSlots & 1, &sh.abort));
+                ok = ok && __all_sync(0xffffffffu, wait_or_abort(&sh.full[s], it / kStages & 1, &sh.abort));
+                if (!ok) break;
+                tc_fence_after();
+                if (scales) ++sc;
+                const uint32_t ta = tmem + kScaleColumn + ((sc - 1) & 1) * 16, tb = ta + 4;
+                if (elect_one()) {
+                    if (scales) {
+                        const uint64_t ds = desc_s + slot * (Sh::kScaleBytes / 16);
+                        tc_copy_scales<kPair>(ta, ds);
+#pragma unroll
+                        for (int p = 0; p < kPanels; ++p) tc_copy_scales<kPair>(tb + 4 * p, ds + 32 * (1 + p));
+                        if (kScales == kScales128) tc_commit<kPair>(&sh.scale_empty[slot]);
+                    }
+                    const uint64_t da = desc_a + s * (Sh::kStageBytes / 16), db = desc_b + s * (Sh::kStageBytes / 16);
+                    // scales of 128: the stage's byte for all four steps; of 32: a byte a step
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        tc_mma_scaled<kPair>(tmem, da + q * (kOuterA ? 256 : 2), db + q * (kOuterB ? 256 : 2),
+                                             with_scale_byte(idesc, kScaleSteps == 4 ? k & 3 : q), ta, tb, k > 0 || q > 0);
+                    tc_commit<kPair>(&sh.empty[s]);
+                    if (k == o.k_tiles - 1) tc_commit<kPair>(&sh.acc_full);
+                }
+                __syncwarp();
+            }
+            ++n;
+        }
+        if (!ok && rank == 0) {   // matrix instructions in flight end before the tensor memory is freed
+            if (elect_one()) tc_commit<kPair>(&sh.drain);
+            __syncwarp();
+            mbar_wait_bounded(&sh.drain, 0, 1ll << 24);
+        }
+    } else if (w < 4) {
+        uint32_t sc = 0;   // slots before this tile; a warp fills every other one
+        const uint32_t half = w & 1;
+        bool ok = kScales == kScales128;
+        for (int t = first; ok && t < total; t += step) {
+            const Tile o = tile_at<kForm, kN, kTileRows>(sh.table, a, t, rank);
+            const int slots = (o.k_tiles + kScaleSteps - 1) / kScaleSteps;
+            constexpr bool kRowsB = kForm == kFormOuter;
+            const int b0 = o.k_base / kTileK;
+            const int last = (kRowsB ? a.rows / kTileK : a.k_tiles) - 1;   // last step whose scales exist
+            const LineSource sa(a.sa, a.sa_row, o.row0, kRowsB ? a.M : a.rows, lane);
+            LineSource sb[kPanels];
+            const uint8_t *sq[kPanels];
+#pragma unroll
+            for (int p = 0; p < kPanels; ++p) {
+                if (kRowsB) sb[p] = LineSource(a.sb, a.sb_row, o.n0 + 128 * p, a.N, lane);
+                else sq[p] = a.sb + o.g * a.sb_group + min(o.n0 / 128 + p, (a.N - 1) / 128) * a.sb_row;
+            }
+            for (int i = (sc ^ half) & 1; i < slots; i += 2) {
+                // the bytes are on their way while the slot is still in use
+                uint32_t ba[16], bb[kPanels][16];
+                sa.load(ba, b0 + 4 * i, last, a.sa_block);
+#pragma unroll
+                for (int p = 0; p < kPanels; ++p) {
+                    if (kRowsB) {
+                        sb[p].load(bb[p], b0 + 4 * i, last, a.sb_block);
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) bb[p][u] = __ldg(sq[p] + min(4 * i + u, last) * a.sb_block);
+                    }
+                }
+                const uint32_t s = (sc + i) % kScaleSlots;
+                ok = wait_or_abort(&sh.scale_empty[s], ((sc + i) / kScaleSlots & 1) ^ 1, &sh.abort);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                uint4 *to = reinterpret_cast<uint4 *>(sh.scales[s]) + lane;
+                to[0] = tile_line(ba);
+#pragma unroll
+                for (int p = 0; p < kPanels; ++p) {
+                    const uint32_t q = four_bytes(bb[p][0], bb[p][1], bb[p][2], bb[p][3]);
+                    to[32 * (1 + p)] = kRowsB ? tile_line(bb[p]) : make_uint4(q, q, q, q);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_at(leader_addr<kPair>(&sh.scale_full[s]));
+            }
+            sc += slots;
+        }
+    } else {
+        const int quarter = w & 3, part = (w - 4) >> 2;   // rows 32 * quarter.., columns part * kN / 2..
+        constexpr int kCols = kN / 2;
         uint32_t n = 0;
         bool ok = true;
-        for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-            const Tile o = tile_at<kForm, kN>(sh.table, a, t);
-            const uint32_t acc = n % kAccs;
-            const bool empty = o.k_tiles == 0;   // a group with no rows: its product is zero
-            if (!empty) {
-                ok = wait_or_abort(&sh.acc_full[acc], n / kAccs & 1, &sh.abort);
+        for (int t = first; ok && t < total; t += step) {
+            const Tile o = tile_at<kForm, kN, kTileRows>(sh.table, a, t, rank);
+            uint32_t v[kCols];
+            if (o.k_tiles > 0) {
+                ok = wait_or_abort(&sh.acc_full, n & 1, &sh.abort);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-            }
-            const int r = quarter * 32 + lane;
-            const int64_t at = (kForm == kFormOuter ? o.g * a.out_group : 0) + (int64_t)(o.row0 + r) * a.out_stride + o.n0;
-            for (int c = 0; c < kN; c += 32) {
-                uint32_t v[32];
-                if (!empty) {
-                    tc_load32(tmem + ((uint32_t)quarter << 21) + acc * kN + c, v);
-                    tc_wait_load();
-                } else {
+                // all of it into registers, so that the next tile can begin
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = 0;
-                }
-                const int valid = min(32, a.N - o.n0 - c);
-                if (r < o.rows && valid > 0) {
-                    if (a.out_type == 0) store_row(static_cast<float *>(a.out) + at + c, v, valid, a.wide_out);
-                    else if (a.out_type == 1) store_row(static_cast<__nv_bfloat16 *>(a.out) + at + c, v, valid, a.wide_out);
-                    else store_row(static_cast<__half *>(a.out) + at + c, v, valid, a.wide_out);
-                }
-            }
-            if (!empty) {
+                for (int c = 0; c < kCols; c += 32)
+                    tc_load32(tmem + ((uint32_t)quarter << 21) + part * kCols + c, v + c);
+                tc_wait_load();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.acc_empty[acc]);
+                if (lane == 0) mbar_arrive_at(leader_addr<kPair>(&sh.acc_empty));
                 ++n;
+            } else {   // a group with no rows: its product is zero
+#pragma unroll
+                for (int i = 0; i < kCols; ++i) v[i] = 0;
+            }
+            const int r0 = quarter * 32, n0 = o.n0 + part * kCols, es = a.out_type == 0 ? 4 : 2;
+            if (a.tma_out && r0 + 32 <= o.rows) {
+                // whole rows of the warp: through shared memory, since a lane holds a row and
+                // 32 rows a store instruction would be 32 separate lines
+                uint8_t *box = sh.out[w - 4];
+#pragma unroll
+                for (int c = 0; c < kCols; c += 16) {
+                    if (es == 2 && c % 32 != 0) continue;
+                    if (n0 + c >= a.N) break;
+                    if (lane == 0) bulk_wait_read<0>();   // the box is free
+                    __syncwarp();
+                    if (a.out_type == 0) stage_row<float>(box, v + c, lane);
+                    else if (a.out_type == 1) stage_row<__nv_bfloat16>(box, v + c, lane);
+                    else stage_row<__half>(box, v + c, lane);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_3d(&maps.out, (n0 + c) * es, o.row0 + r0, kForm == kFormOuter ? o.g : 0, box);
+                        bulk_commit();
+                    }
+                }
+            } else if (r0 + lane < o.rows) {
+                const int64_t at = (kForm == kFormOuter ? o.g * a.out_group : 0) + (int64_t)(o.row0 + r0 + lane) * a.out_stride + n0;
+#pragma unroll
+                for (int c = 0; c < kCols; c += 32) {
+                    uint32_t u[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) u[i] = v[c + i];
+                    if (a.out_type == 0) store_row<float>(a.out, at + c, u, a.N - n0 - c);
+                    else if (a.out_type == 1) store_row<__nv_bfloat16>(a.out, at + c, u, a.N - n0 - c);
+                    else store_row<__half>(a.out, at + c, u, a.N - n0 - c);
+                }
             }
         }
+        if (lane == 0) bulk_wait_all();
         if (kForm != kFormOuter) {   // rows behind the last group
-            const int last = sh.table.begin[a.G - 1] + sh.table.size[a.G - 1];
-            const int64_t cells = (int64_t)(a.rows - last) * a.N;
-            for (int64_t i = (int64_t)blockIdx.x * 128 + (tid - 128); i < cells; i += (int64_t)gridDim.x * 128) {
-                const int64_t r = i / a.N, at = (last + r) * a.out_stride + (i - r * a.N);
-                if (a.out_type == 0) static_cast<float *>(a.out)[at] = 0.f;
-                else static_cast<uint16_t *>(a.out)[at] = 0;
+            const int es = a.out_type == 0 ? 4 : 2;
+            const int64_t bytes = (int64_t)a.N * es;
+            int64_t r = sh.table.begin[a.G - 1] + sh.table.size[a.G - 1] + (int64_t)blockIdx.x * kDrainWarps + (w - 4);
+            for (; r < a.rows; r += (int64_t)gridDim.x * kDrainWarps) {
+                uint8_t *row = static_cast<uint8_t *>(a.out) + r * a.out_stride * es;
+                int64_t i = 0;
+                if (a.tma_out) {
+                    i = bytes & ~int64_t(15);
+                    for (int64_t b = lane * 16; b < i; b += 512) *reinterpret_cast<uint4 *>(row + b) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                for (i += lane * 2; i < bytes; i += 64) *reinterpret_cast<uint16_t *>(row + i) = 0;
             }
         }
     }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (kPair) cluster_sync();   // neither CTA leaves while the other may signal it or read its shared memory
     tc_fence_after();
-    if (w == 3) tmem_free(tmem, kTmemColumns);
+    if (w == 3) tmem_free<kPair>(tmem, kTmemColumns);
 }
 
 // ------------------------------------------------------------------ host side
 constexpr int kMatMaxDevices = 128;
 
-template <int kForm, int kScales, int kN>
-mx_status launch_product(const CUtensorMap &ma, const CUtensorMap &mb, const MatArgs &a, int64_t tiles, cudaStream_t stream) {
-    constexpr int smem = (int)sizeof(Shared<kN>) + 1024;
-    auto kernel = grouped_product<kForm, kScales, kN>;
+template <int kForm, int kScales, int kN, bool kPair>
+mx_status launch_product(const Maps &maps, MatArgs a, cudaStream_t stream) {
+    using Sh = Shared<kScales, kN, kPair>;
+    constexpr int smem = (int)sizeof(Sh) + 1024, kCtas = kPair ? 2 : 1;
+    auto kernel = grouped_product<kForm, kScales, kN, kPair>;
+    a.n_tiles = (int32_t)div_up(a.N, kN);
+    a.m_tiles = (int32_t)div_up(a.M, Sh::kTileRows);
+    a.n_first = a.N % kN != 0 && a.N % kN <= kN / 2 ? a.n_tiles - 1 : a.n_tiles;
+    // an upper bound on the tiles, known without the group ends
+    const int64_t tiles = kForm == kFormOuter ? (int64_t)a.m_tiles * a.n_tiles * a.G
+                                              : (div_up(a.rows, Sh::kTileRows) + a.G) * a.n_tiles;
+    if (tiles > INT_MAX / 2) return MX_ERR_UNSUPPORTED;
+
     static std::mutex mu;
-    static bool ready[kMatMaxDevices] = {};
-    int dev = 0;
+    static int resident[kMatMaxDevices] = {};   // CTAs, or pairs, that run at once
+    int dev = 0, sms = 0;
+    if (mx_status st = mx_device_sms(&sms); st != MX_OK) return st;
     if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return mx_record_cuda_error(e);
     if (dev < 0 || dev >= kMatMaxDevices) return MX_ERR_UNSUPPORTED;
-    int sms = 0;
-    if (mx_status st = mx_device_sms(&sms); st != MX_OK) return st;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kCtas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.blockDim = dim3(kMatThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = kPair ? 1 : 0;
+    int most;
     {
         std::lock_guard<std::mutex> lock(mu);
-        if (!ready[dev]) {
+        if (resident[dev] == 0) {
             if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); e != cudaSuccess)
                 return mx_record_cuda_error(e);
-            ready[dev] = true;
+            int n = sms;
+            if (kPair) {
+                cfg.gridDim = dim3(sms / 2 * 2);
+                if (cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg); e != cudaSuccess || n < 1)
+                    return mx_record_cuda_error(e != cudaSuccess ? e : cudaErrorInvalidConfiguration);
+            }
+            resident[dev] = n;
         }
+        most = resident[dev];
     }
-    return launch(kernel, tiles < sms ? tiles : sms, kMatThreads, smem, stream, ma, mb, a);
+    cfg.gridDim = dim3((unsigned)((tiles < most ? tiles : most) * kCtas));
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, maps, a);
+    return e == cudaSuccess ? MX_OK : mx_record_cuda_error(e);
+}
+
+// Operand bytes as the loads take them: contraction inner, 128 of it and
+// `rows` rows a box; contraction outer, 128 columns and 128 rows a box.
+mx_status operand_map(CUtensorMap *map, const void *p, int64_t inner, int64_t outer, int64_t stride, int64_t groups,
+                      int64_t group_stride, uint32_t rows) {
+    const uint64_t dims[3] = {(uint64_t)inner, (uint64_t)outer, (uint64_t)groups};
+    const uint64_t strides[2] = {(uint64_t)stride, (uint64_t)group_stride};
+    const uint32_t box[3] = {128, rows, 1};
+    return mx_encode_map(map, p, groups > 0 ? 3 : 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// 512-byte tiles of blocked scales.
+mx_status tiles_map(CUtensorMap *map, const void *p, int64_t tiles) {
+    const uint64_t dims[2] = {128, (uint64_t)tiles}, strides[1] = {512};
+    const uint32_t box[2] = {128, 1};
+    return mx_encode_map(map, p, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+// The output in bytes, 32 rows x 64 bytes a box.
+mx_status out_map(CUtensorMap *map, const void *p, int64_t row_bytes, int64_t rows, int64_t stride, int64_t groups, int64_t group_stride) {
+    const uint64_t dims[3] = {(uint64_t)row_bytes, (uint64_t)rows, (uint64_t)groups};
+    const uint64_t strides[2] = {(uint64_t)stride, (uint64_t)group_stride};
+    const uint32_t box[3] = {kOutRow, 32, 1};
+    return mx_encode_map(map, p, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 int out_code(mx_dtype t) { return t == MX_F32 ? 0 : t == MX_BF16 ? 1 : t == MX_F16 ? 2 : -1; }
 bool eight(mx_dtype t) { return t == MX_E4M3 || t == MX_E5M2; }
+
+bool use_pair(int64_t rows_of_group) {
+    return rows_of_group > 128;
+}
 
 bool operand_ok(const void *p, int64_t stride) { return aligned_to(p, 16) && stride % 16 == 0; }
 
@@ -478,27 +624,32 @@ mx_status mx_grouped_matmul_m(const void *a, mx_dtype a_dtype, int64_t a_stride,
     m.G = num_groups;
     m.rows = (int32_t)rows;
     m.N = (int32_t)n;
-    m.K = (int32_t)k;
     m.k_tiles = (int32_t)div_up(k, kTileK);
     m.out_type = out_code(out_dtype);
-    m.wide_out = aligned_to(out, 16) && (out_stride * os) % 16 == 0;
-    const int tile_n = 256;
-    m.n_tiles = (int32_t)div_up(n, tile_n);
-    m.idesc = block_scaled_idesc(a_dtype == MX_E5M2, b_dtype == MX_E5M2, false, !nk, kTileM, tile_n);
-    const int64_t tiles = (div_up(rows, kTileM) + num_groups) * m.n_tiles;
-    if (tiles > INT_MAX / 2) return MX_ERR_UNSUPPORTED;
-
-    CUtensorMap ma, mb;
-    const uint64_t da[2] = {(uint64_t)k, (uint64_t)rows}, sa[1] = {(uint64_t)a_stride};
-    const uint32_t ba[2] = {128, 128};
-    if (mx_status st = mx_encode_bytes_map(&ma, a, 2, da, sa, ba); st != MX_OK) return st;
-    const uint64_t db[3] = {(uint64_t)(nk ? k : n), (uint64_t)(nk ? n : k), (uint64_t)num_groups};
-    const uint64_t sb[2] = {(uint64_t)b_stride, (uint64_t)(num_groups > 1 ? b_group_stride : b_stride)};
-    const uint32_t bb[3] = {128, nk ? (uint32_t)tile_n : 128u, 1};
-    if (mx_status st = mx_encode_bytes_map(&mb, b, 3, db, sb, bb); st != MX_OK) return st;
-    if (block == 32) return launch_product<kFormNK, kScales32, 256>(ma, mb, m, tiles, stream);
-    if (nk) return launch_product<kFormNK, kScales128, 256>(ma, mb, m, tiles, stream);
-    return launch_product<kFormKN, kScales128, 256>(ma, mb, m, tiles, stream);
+    m.tma_out = aligned_to(out, 16) && (out_stride * os) % 16 == 0;
+    m.idesc = block_scaled_idesc(a_dtype == MX_E5M2, b_dtype == MX_E5M2, false, !nk);
+    const bool pair = use_pair(div_up(rows, num_groups));
+    Maps maps = {};
+    if (mx_status st = operand_map(&maps.a, a, k, rows, a_stride, 0, 0, 128); st != MX_OK) return st;
+    if (mx_status st = operand_map(&maps.b, b, nk ? k : n, nk ? n : k, b_stride, num_groups,
+                                   num_groups > 1 ? b_group_stride : b_stride, nk && !pair ? 256 : 128);
+        st != MX_OK)
+        return st;
+    if (m.tma_out)
+        if (mx_status st = out_map(&maps.out, out, n * os, rows, out_stride * os, 1, out_stride * os); st != MX_OK) return st;
+    if (block == 32) {
+        const int64_t a_tiles = (rows + 128ll * num_groups) / 128 * m.k_tiles, b_tiles = num_groups * div_up(n, 128) * m.k_tiles;
+        if (a_tiles > INT_MAX || b_tiles > INT_MAX) return MX_ERR_UNSUPPORTED;
+        if (mx_status st = tiles_map(&maps.sa, a_scales, a_tiles); st != MX_OK) return st;
+        if (mx_status st = tiles_map(&maps.sb, b_scales, b_tiles); st != MX_OK) return st;
+        return pair ? launch_product<kFormNK, kScales32, 256, true>(maps, m, stream)
+                    : launch_product<kFormNK, kScales32, 256, false>(maps, m, stream);
+    }
+    if (nk)
+        return pair ? launch_product<kFormNK, kScales128, 256, true>(maps, m, stream)
+                    : launch_product<kFormNK, kScales128, 256, false>(maps, m, stream);
+    return pair ? launch_product<kFormKN, kScales128, 256, true>(maps, m, stream)
+                : launch_product<kFormKN, kScales128, 256, false>(maps, m, stream);
 }
 
 mx_status mx_grouped_matmul_k(const void *a, mx_dtype a_dtype, int64_t a_stride, const uint8_t *a_scales,
@@ -536,21 +687,18 @@ mx_status mx_grouped_matmul_k(const void *a, mx_dtype a_dtype, int64_t a_stride,
     g.M = (int32_t)m;
     g.N = (int32_t)n;
     g.out_type = out_code(out_dtype);
-    g.wide_out = aligned_to(out, 16) && (out_stride * os) % 16 == 0 && (g.out_group * os) % 16 == 0;
-    const int tile_n = 256;
-    g.n_tiles = (int32_t)div_up(n, tile_n);
-    g.m_tiles = (int32_t)div_up(m, kTileM);
-    g.idesc = block_scaled_idesc(a_dtype == MX_E5M2, b_dtype == MX_E5M2, true, true, kTileM, tile_n);
-    const int64_t tiles = (int64_t)g.m_tiles * g.n_tiles;
-    if (tiles > INT_MAX / 2 / num_groups) return MX_ERR_UNSUPPORTED;
-
-    CUtensorMap ma, mb;
-    const uint64_t da[2] = {(uint64_t)m, (uint64_t)padded_rows}, sa[1] = {(uint64_t)a_stride};
-    const uint64_t db[2] = {(uint64_t)n, (uint64_t)padded_rows}, sb[1] = {(uint64_t)b_stride};
-    const uint32_t box[2] = {128, 128};
-    if (mx_status st = mx_encode_bytes_map(&ma, a, 2, da, sa, box); st != MX_OK) return st;
-    if (mx_status st = mx_encode_bytes_map(&mb, b, 2, db, sb, box); st != MX_OK) return st;
-    return launch_product<kFormOuter, kScales128, 256>(ma, mb, g, tiles * num_groups, stream);
+    g.tma_out = aligned_to(out, 16) && (out_stride * os) % 16 == 0 && (g.out_group * os) % 16 == 0;
+    g.idesc = block_scaled_idesc(a_dtype == MX_E5M2, b_dtype == MX_E5M2, true, true);
+    Maps maps = {};
+    if (mx_status st = operand_map(&maps.a, a, m, padded_rows, a_stride, 0, 0, 128); st != MX_OK) return st;
+    if (mx_status st = operand_map(&maps.b, b, n, padded_rows, b_stride, 0, 0, 128); st != MX_OK) return st;
+    if (g.tma_out)
+        if (mx_status st = out_map(&maps.out, out, n * os, m, out_stride * os, num_groups,
+                                   (num_groups > 1 ? out_group_stride : out_stride) * os);
+            st != MX_OK)
+            return st;
+    return use_pair(m) ? launch_product<kFormOuter, kScales128, 256, true>(maps, g, stream)
+                       : launch_product<kFormOuter, kScales128, 256, false>(maps, g, stream);
 }
 
 }  // extern "C"

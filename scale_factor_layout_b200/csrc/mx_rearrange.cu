@@ -941,10 +941,11 @@ mx_status mx_device_sms(int *sms) {
     return MX_OK;
 }
 
-// A tensor map over bytes of `rank` 2 or 3 with the 128-byte swizzle, for the
-// current device; strides[i] is that of dimension i + 1, boxes are 128 bytes wide.
-mx_status mx_encode_bytes_map(CUtensorMap *map, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
-                              const uint32_t *box) {
+// A tensor map of `rank` 2 or 3 for the current device, over bytes with a
+// swizzle, or over 32-bit words where there is none; strides[i] is that of
+// dimension i + 1, in bytes.
+mx_status mx_encode_map(CUtensorMap *map, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
+                        const uint32_t *box, CUtensorMapSwizzle swizzle) {
     const mx::DeviceInfo *d = nullptr;
     if (mx_status st = mx::device_info(&d); st != MX_OK) return st;
     auto encode = mx::encode_fn();
@@ -953,9 +954,10 @@ mx_status mx_encode_bytes_map(CUtensorMap *map, const void *base, int rank, cons
     cuuint64_t gdim[3], gstride[2];
     for (int i = 0; i < rank; ++i) gdim[i] = dims[i];
     for (int i = 0; i + 1 < rank; ++i) gstride[i] = strides[i];
-    CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void *>(base), gdim, gstride, box, estride,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const bool words = swizzle == CU_TENSOR_MAP_SWIZZLE_NONE;
+    CUresult r = encode(map, words ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT8, rank,
+                        const_cast<void *>(base), gdim, gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? MX_OK : mx::cuda_status(static_cast<cudaError_t>(r));   // driver code
 }
 

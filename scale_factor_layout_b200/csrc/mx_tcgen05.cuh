@@ -17,52 +17,121 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
 
 // Instruction descriptor of a block-scaled 8-bit product with E8M0 scales:
 // operand types (0 e4m3, 1 e5m2), majors (1: the contraction is the outer
-// dimension), N / 8, scale type, M / 16.  The scales' byte within a 32-bit
-// column is added by with_scale_byte.
-__host__ __device__ constexpr uint32_t block_scaled_idesc(uint32_t a_type, uint32_t b_type, bool a_outer, bool b_outer,
-                                                          uint32_t M, uint32_t N) {
-    return a_type << 7 | b_type << 10 | (uint32_t)a_outer << 15 | (uint32_t)b_outer << 16 | (N / 8) << 17 | 1u << 23 |
-           (M / 16) << 24;
+// dimension) and scale type; the launch adds N / 8 at bit 17 and M / 16 at bit
+// 24.  The scales' byte within a 32-bit column is added by with_scale_byte.
+inline uint32_t block_scaled_idesc(bool a_e5m2, bool b_e5m2, bool a_outer, bool b_outer) {
+    return (uint32_t)a_e5m2 << 7 | (uint32_t)b_e5m2 << 10 | (uint32_t)a_outer << 15 | (uint32_t)b_outer << 16 | 1u << 23;
 }
 __device__ __forceinline__ uint32_t with_scale_byte(uint32_t idesc, uint32_t byte) {
     return idesc | byte << 4 | byte << 29;
 }
 
-// ------------------------------------------------------------------ tensor memory
-__device__ __forceinline__ void tmem_alloc(uint32_t *where, uint32_t columns) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-                 ::"r"(smem_addr(where)), "r"(columns) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+// One lane of a converged warp.  The tensor core and copy instructions take
+// their operands from the warp's uniform registers; under this predicate the
+// compiler knows that a single lane is left, which under `lane == 0` it does not.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
 }
+
+// ------------------------------------------------------------------ pairs
+// kPair: two CTAs of a cluster work on one tile; the matrix instructions and
+// scale copies are issued by the one of rank 0 and run in both.
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of this CTA's shared variable in the CTA of rank 0, or here.
+template <bool kPair>
+__device__ __forceinline__ uint32_t leader_addr(const void *p) {
+    const uint32_t here = smem_addr(p);
+    if (!kPair) return here;
+    uint32_t there;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(there) : "r"(here));
+    return there;
+}
+// Arrivals on a barrier of either CTA of the pair.  What they order is read by
+// the tensor cores and the copy engine, not by threads: scale bytes by a proxy
+// fence before the arrival, tensor memory by the tcgen05 fences, operand bytes
+// by the barrier's own count.  So the arrivals carry no cluster-wide release,
+// and the waits no cluster-wide acquire: on a B200 those took the 128 x 256
+// loop from about 1100 to 2000 clocks a stage.
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_at(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// ------------------------------------------------------------------ tensor memory
+template <bool kPair>
+__device__ __forceinline__ void tmem_alloc(uint32_t *where, uint32_t columns) {
+    if (kPair) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_addr(where)), "r"(columns) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_addr(where)), "r"(columns) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+}
+template <bool kPair>
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
+    if (kPair) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
+    else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// Arrive on `bar` once every matrix instruction and scale copy issued by this
-// thread has completed.
+// Arrive on `bar` (of both CTAs of a pair) once every matrix instruction and
+// scale copy issued by this thread has completed.
+template <bool kPair>
 __device__ __forceinline__ void tc_commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-                 ::"r"(smem_addr(bar)) : "memory");
+    if (kPair)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                     ::"r"(smem_addr(bar)), "h"((uint16_t)3) : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                     ::"r"(smem_addr(bar)) : "memory");
 }
 
-// 32 rows x 16 bytes of shared memory into 4 columns, in all four lane quarters.
+// 32 rows x 16 bytes of shared memory into 4 columns, in all four lane
+// quarters (each CTA of a pair from its own shared memory into its own columns).
+template <bool kPair>
 __device__ __forceinline__ void tc_copy_scales(uint32_t tmem, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+    if (kPair) asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+    else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
 }
 
+template <bool kPair>
 __device__ __forceinline__ void tc_mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t scale_a,
                                               uint32_t scale_b, bool accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(scale_a), "r"(scale_b) : "memory");
+    if (kPair)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(scale_a), "r"(scale_b) : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(scale_a), "r"(scale_b) : "memory");
 }
 
 // 32 consecutive columns of this warp's 32 lanes: lane l gets row l's values.
-__device__ __forceinline__ void tc_load32(uint32_t addr, uint32_t (&v)[32]) {
+__device__ __forceinline__ void tc_load32(uint32_t addr, uint32_t *v) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -76,23 +145,40 @@ __device__ __forceinline__ void tc_load32(uint32_t addr, uint32_t (&v)[32]) {
 __device__ __forceinline__ void tc_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // ------------------------------------------------------------------ copies
-__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];"
-        ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
-        : "memory");
+// Tiled loads into this CTA's shared memory; the bytes are signalled on `bar`,
+// in a pair that of the CTA of rank 0.
+template <bool kPair>
+__device__ __forceinline__ void tma_load_2d_to(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    if (kPair)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3}], [%4];"
+            ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar) : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3}], [%4];"
+            ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+template <bool kPair>
+__device__ __forceinline__ void tma_load_3d_to(void *dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
+    if (kPair)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4}], [%5];"
+            ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4}], [%5];"
+            ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
 }
 
-// `bytes` (a multiple of 16) from 16-byte aligned global to shared memory.
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_addr(bar))
-                 : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+// A box of shared memory into a tensor, parts outside it left out; tracked in
+// bulk groups.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, int x, int y, int z, const void *src) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(src)) : "memory");
 }
 
 }  // namespace mx
