@@ -208,10 +208,10 @@ __device__ __forceinline__ void stage_row(uint8_t *box, const uint32_t *v, int l
     constexpr int N = 16 / sizeof(T);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-        Pack<T, N> p;
+        float f[N];
 #pragma unroll
-        for (int u = 0; u < N; ++u) p.v[u] = from_f32<T>(__uint_as_float(v[c * N + u]));
-        *reinterpret_cast<Pack<T, N> *>(box + lane * kOutRow + ((c ^ (lane >> 1 & 3)) << 4)) = p;
+        for (int u = 0; u < N; ++u) f[u] = __uint_as_float(v[c * N + u]);
+        *reinterpret_cast<uint4 *>(box + lane * kOutRow + ((c ^ (lane >> 1 & 3)) << 4)) = pack<T, N>(f);
     }
 }
 

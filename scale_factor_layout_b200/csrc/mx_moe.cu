@@ -209,7 +209,7 @@ template <typename T, int N>
 __global__ void __launch_bounds__(kRowThreads)
 combine_kernel(const T *__restrict__ rows, int64_t rows_stride, const int *__restrict__ row_of_slot,
                const float *__restrict__ weights, T *__restrict__ y, int64_t y_stride, RowShape s) {
-    using P = Pack<T, N>;
+    using P = Raw<T, N>;
     grid_dependency_wait();
     const int64_t slab = blockIdx.x / s.chunks;
     const int chunk = (int)(blockIdx.x - slab * s.chunks);
@@ -238,14 +238,13 @@ combine_kernel(const T *__restrict__ rows, int64_t rows_stride, const int *__res
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
             if (live[u]) {
+                float f[N];
+                unpack<T, N>(v[u], f);
 #pragma unroll
-                for (int i = 0; i < N; ++i) sum[i] = fmaf(w[u], to_f32(v[u].v[i]), sum[i]);
+                for (int i = 0; i < N; ++i) sum[i] = fmaf(w[u], f[i], sum[i]);
             }
     }
-    P o;
-#pragma unroll
-    for (int i = 0; i < N; ++i) o.v[i] = from_f32<T>(sum[i]);
-    *reinterpret_cast<P *>(y + t * y_stride + (int64_t)p * N) = o;
+    *reinterpret_cast<P *>(y + t * y_stride + (int64_t)p * N) = pack<T, N>(sum);
 }
 
 // d_rows[row_of_slot[t, j]] = w[t, j] * grad[t]; d_weights[t, j] = <grad[t], rows[...]>.
@@ -257,7 +256,7 @@ combine_backward_kernel(const T *__restrict__ grad, int64_t grad_stride, const T
                         int64_t rows_stride, const int *__restrict__ row_of_slot, const int *__restrict__ last_end,
                         const float *__restrict__ weights, T *__restrict__ d_rows, int64_t d_rows_stride,
                         float *__restrict__ d_weights, RowShape s) {
-    using P = Pack<T, N>;
+    using P = Raw<T, N>;
     constexpr int kAhead = 8;
     __shared__ float part[kRowThreads / 32][kAhead];
     grid_dependency_wait();
@@ -278,7 +277,8 @@ combine_backward_kernel(const T *__restrict__ grad, int64_t grad_stride, const T
                 dot[u] = 0.f;
             }
             for (int p = threadIdx.x % kTpt; p < s.packs; p += kTpt) {
-                const P g = *reinterpret_cast<const P *>(grad + t * grad_stride + (int64_t)p * N);
+                float g[N];
+                unpack<T, N>(*reinterpret_cast<const P *>(grad + t * grad_stride + (int64_t)p * N), g);
                 P v[kAhead];
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u)
@@ -286,14 +286,14 @@ combine_backward_kernel(const T *__restrict__ grad, int64_t grad_stride, const T
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u)
                     if (live[u]) {
-                        P o;
+                        float f[N], o[N];
+                        unpack<T, N>(v[u], f);
 #pragma unroll
                         for (int i = 0; i < N; ++i) {
-                            const float gi = to_f32(g.v[i]);
-                            dot[u] = fmaf(gi, to_f32(v[u].v[i]), dot[u]);
-                            o.v[i] = from_f32<T>(wt[u] * gi);
+                            dot[u] = fmaf(g[i], f[i], dot[u]);
+                            o[i] = wt[u] * g[i];
                         }
-                        *reinterpret_cast<P *>(d_rows + at[u] * d_rows_stride + (int64_t)p * N) = o;
+                        *reinterpret_cast<P *>(d_rows + at[u] * d_rows_stride + (int64_t)p * N) = pack<T, N>(o);
                     }
             }
 #pragma unroll

@@ -37,16 +37,61 @@ mx_status launch(void (*kernel)(KArgs...), int64_t grid, int block, int smem, cu
     return e == cudaSuccess ? MX_OK : mx_record_cuda_error(e);
 }
 
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 template <typename T> __device__ __forceinline__ T from_f32(float v);
 template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
-// N consecutive elements moved by one load or store (16 bytes, or one element
-// where rows do not start on 16-byte boundaries).
-template <typename T, int N> struct alignas(sizeof(T) * N) Pack { T v[N]; };
+// N consecutive elements as one load or store moves them: 16 bytes, or one
+// element where rows do not start on 16-byte boundaries.  They stay words until
+// they are unpacked: arrays of 16-bit types are not always moved as a whole.
+template <typename T, int N> struct RawOf { using Type = uint4; };
+template <> struct RawOf<float, 1> { using Type = uint32_t; };
+template <> struct RawOf<__nv_bfloat16, 1> { using Type = uint16_t; };
+template <> struct RawOf<__half, 1> { using Type = uint16_t; };
+template <typename T, int N> using Raw = typename RawOf<T, N>::Type;
+
+template <typename T> __device__ __forceinline__ float2 two_floats(uint32_t w);
+template <> __device__ __forceinline__ float2 two_floats<__nv_bfloat16>(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <> __device__ __forceinline__ float2 two_floats<__half>(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+template <typename T> __device__ __forceinline__ uint32_t two_packed(float lo, float hi);
+template <> __device__ __forceinline__ uint32_t two_packed<__nv_bfloat16>(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <> __device__ __forceinline__ uint32_t two_packed<__half>(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void unpack(const Raw<T, N> &r, float (&f)[N]) {
+    if constexpr (N == 1 && sizeof(T) == 4) {
+        f[0] = __uint_as_float(r);
+    } else if constexpr (N == 1) {
+        f[0] = two_floats<T>(r).x;
+    } else if constexpr (sizeof(T) == 4) {
+        f[0] = __uint_as_float(r.x), f[1] = __uint_as_float(r.y), f[2] = __uint_as_float(r.z), f[3] = __uint_as_float(r.w);
+    } else {
+        const float2 a = two_floats<T>(r.x), b = two_floats<T>(r.y), c = two_floats<T>(r.z), d = two_floats<T>(r.w);
+        f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y, f[4] = c.x, f[5] = c.y, f[6] = d.x, f[7] = d.y;
+    }
+}
+template <typename T, int N>
+__device__ __forceinline__ Raw<T, N> pack(const float (&f)[N]) {
+    if constexpr (N == 1 && sizeof(T) == 4) {
+        return __float_as_uint(f[0]);
+    } else if constexpr (N == 1) {
+        return (uint16_t)two_packed<T>(f[0], 0.f);
+    } else if constexpr (sizeof(T) == 4) {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    } else {
+        return make_uint4(two_packed<T>(f[0], f[1]), two_packed<T>(f[2], f[3]), two_packed<T>(f[4], f[5]), two_packed<T>(f[6], f[7]));
+    }
+}
 
 }  // namespace mx

@@ -53,25 +53,48 @@ __device__ __forceinline__ uint2 eight_bits(const float (&v)[8], uint32_t byte, 
     return q;
 }
 
-// Eight consecutive elements of a row from column c on, zeros past `cols`.
-// kWide: rows start on 16-byte boundaries and cols is a multiple of 8.
+// Eight consecutive elements of a row from column c on, zeros past `cols`, as
+// the words that hold them.  kWide: rows start on 16-byte boundaries and cols is
+// a multiple of 8.
+template <typename T> struct Eight { uint4 q[sizeof(T) / 2]; };
 template <typename T, bool kWide>
-__device__ __forceinline__ Pack<T, 8> load8(const T *row, int c, int cols) {
-    Pack<T, 8> v;
+__device__ __forceinline__ Eight<T> load8(const T *row, int c, int cols) {
+    Eight<T> v;
     if (kWide) {
-        if (c < cols) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(row + c);
-            uint4 *dst = reinterpret_cast<uint4 *>(&v);
 #pragma unroll
-            for (int i = 0; i < (int)sizeof(T) / 2; ++i) dst[i] = __ldg(src + i);
-        } else {
-            memset(&v, 0, sizeof(v));
-        }
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+            v.q[i] = c < cols ? __ldg(reinterpret_cast<const uint4 *>(row + c) + i) : make_uint4(0u, 0u, 0u, 0u);
     } else {
+        using W = Raw<T, 1>;
+        const W *src = reinterpret_cast<const W *>(row);
+        uint32_t e[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v.v[i] = c + i < cols ? row[c + i] : from_f32<T>(0.f);
+        for (int i = 0; i < 8; ++i) e[i] = c + i < cols ? src[c + i] : 0u;
+        if constexpr (sizeof(T) == 4) {
+            v.q[0] = make_uint4(e[0], e[1], e[2], e[3]);
+            v.q[1] = make_uint4(e[4], e[5], e[6], e[7]);
+        } else {
+            v.q[0] = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+        }
     }
     return v;
+}
+template <typename T> __device__ __forceinline__ Eight<T> no_eight() {
+    Eight<T> v;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) v.q[i] = make_uint4(0u, 0u, 0u, 0u);
+    return v;
+}
+template <typename T> __device__ __forceinline__ void floats_of(const Eight<T> &v, float (&f)[8]) {
+    if constexpr (sizeof(T) == 4) {
+        float lo[4], hi[4];
+        unpack<T, 4>(v.q[0], lo);
+        unpack<T, 4>(v.q[1], hi);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = lo[i], f[4 + i] = hi[i];
+    } else {
+        unpack<T, 8>(v.q[0], f);
+    }
 }
 
 template <bool kWide>
@@ -110,21 +133,18 @@ quantize_rows_kernel(const T *__restrict__ x, int64_t x_stride, RowsArgs a) {
     const int c = (int)(blockIdx.x - band * a.segments) * 256 + lane * 8;
     const int64_t r0 = band * 32 + w * 4;
     const int fexp = a.e5m2 ? 15 : 8;
-    Pack<T, 8> v[4];
+    Eight<T> v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if (r0 + i < a.in_rows) v[i] = load8<T, kWide>(x + (r0 + i) * x_stride, c, a.cols);
-        else memset(&v[i], 0, sizeof(v[i]));
+        v[i] = r0 + i < a.in_rows ? load8<T, kWide>(x + (r0 + i) * x_stride, c, a.cols) : no_eight<T>();
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         float f[8];
+        floats_of(v[i], f);
         uint32_t amax = 0;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            f[u] = to_f32(v[i].v[u]);
-            amax = max(amax, magnitude(f[u]));
-        }
+        for (int u = 0; u < 8; ++u) amax = max(amax, magnitude(f[u]));
 #pragma unroll
         for (int d = 1; d < kBlock / 8; d <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, d));
         const uint32_t byte = scale_byte(amax, fexp);
@@ -214,20 +234,22 @@ quantize_tiles_kernel(const T *__restrict__ x, TileArgs a) {
             dst += p * a.q_stride;
             scale_at = rb * a.scale_stride + c0;
         }
-        Pack<T, 8> v[8];
+        Eight<T> v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int r = ty + 16 * i;
-            if (r < valid) v[i] = load8<T, kWide>(src + r * a.x_stride, c, a.cols);
-            else memset(&v[i], 0, sizeof(v[i]));
+            v[i] = r < valid ? load8<T, kWide>(src + r * a.x_stride, c, a.cols) : no_eight<T>();
         }
         uint32_t m[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) m[u] = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 8; ++i) {
+            float f[8];
+            floats_of(v[i], f);
 #pragma unroll
-            for (int u = 0; u < 8; ++u) m[u] = max(m[u], magnitude(to_f32(v[i].v[u])));
+            for (int u = 0; u < 8; ++u) m[u] = max(m[u], magnitude(f[u]));
+        }
         if (kSquare) {
             uint32_t all = 0;
 #pragma unroll
@@ -269,8 +291,9 @@ quantize_tiles_kernel(const T *__restrict__ x, TileArgs a) {
         for (int i = 0; i < 8; ++i) {
             const int r = ty + 16 * i;
             float f[8];
+            floats_of(v[i], f);
 #pragma unroll
-            for (int u = 0; u < 8; ++u) f[u] = to_f32(v[i].v[u]) * s[u];
+            for (int u = 0; u < 8; ++u) f[u] *= s[u];
             uint2 q;
             q.x = two_eight_bit(f[0], f[1], a.e5m2) | two_eight_bit(f[2], f[3], a.e5m2) << 16;
             q.y = two_eight_bit(f[4], f[5], a.e5m2) | two_eight_bit(f[6], f[7], a.e5m2) << 16;
