@@ -28,8 +28,6 @@ constexpr uint32_t kInfBits = 0x7f800000u;
 
 // Magnitudes are compared as bits: the order of finite values is that of their
 // bits, and infinities and NaNs lie above all of them.
-__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
-
 __device__ __forceinline__ uint32_t scale_byte(uint32_t amax, int fexp) {
     if (amax >= kInfBits) return 255u;
     const int b = (int)(amax >> 23) - fexp + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0);
@@ -39,19 +37,17 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax, int fexp) {
 // 2^-e of a finite scale byte: its exponent field is 254 - byte, 7 .. 254.
 __device__ __forceinline__ float inverse_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 
-__device__ __forceinline__ uint32_t two_eight_bit(float lo, float hi, bool e5m2) {
-    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, e5m2 ? __NV_E5M2 : __NV_E4M3);
+template <__nv_fp8_interpretation_t kTo>
+__device__ __forceinline__ uint2 eight_bytes(const float (&v)[8]) {
+    uint32_t p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, kTo);
+    return make_uint2(p[0] | p[1] << 16, p[2] | p[3] << 16);
 }
-
-// Eight values as 8 bytes; 0x7f is a NaN in both types.
-__device__ __forceinline__ uint2 eight_bits(const float (&v)[8], uint32_t byte, bool e5m2) {
-    if (byte == 255u) return make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
-    const float s = inverse_scale(byte);
-    uint2 q;
-    q.x = two_eight_bit(v[0] * s, v[1] * s, e5m2) | two_eight_bit(v[2] * s, v[3] * s, e5m2) << 16;
-    q.y = two_eight_bit(v[4] * s, v[5] * s, e5m2) | two_eight_bit(v[6] * s, v[7] * s, e5m2) << 16;
-    return q;
+__device__ __forceinline__ uint2 eight_bytes(const float (&v)[8], bool e5m2) {
+    return e5m2 ? eight_bytes<__NV_E5M2>(v) : eight_bytes<__NV_E4M3>(v);
 }
+constexpr uint32_t kNanBytes = 0x7f7f7f7fu;   // four NaNs in both types
 
 // Eight consecutive elements of a row from column c on, zeros past `cols`, as
 // the words that hold them.  kWide: rows start on 16-byte boundaries and cols is
@@ -94,6 +90,47 @@ template <typename T> __device__ __forceinline__ void floats_of(const Eight<T> &
         for (int i = 0; i < 4; ++i) f[i] = lo[i], f[4 + i] = hi[i];
     } else {
         unpack<T, 8>(v.q[0], f);
+    }
+}
+
+// The largest magnitudes so far, as bits: two 16-bit ones a word (their order is
+// that of their bits too), or one of 32 bits.
+template <typename T> struct Top { uint32_t w[sizeof(T) == 4 ? 8 : 4] = {}; };
+template <typename T> __device__ __forceinline__ void raise(Top<T> &t, const Eight<T> &v) {
+    if constexpr (sizeof(T) == 4) {
+        const uint32_t e[8] = {v.q[0].x, v.q[0].y, v.q[0].z, v.q[0].w, v.q[1].x, v.q[1].y, v.q[1].z, v.q[1].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t.w[i] = max(t.w[i], e[i] & 0x7fffffffu);
+    } else {
+        const uint32_t e[4] = {v.q[0].x, v.q[0].y, v.q[0].z, v.q[0].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t.w[i] = __vmaxu2(t.w[i], e[i] & 0x7fff7fffu);
+    }
+}
+// Each column's, as bits of a 32-bit float.
+template <typename T> __device__ __forceinline__ void columns_of(const Top<T> &t, uint32_t (&m)[8]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m[i] = t.w[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = two_floats<T>(t.w[i]);
+            m[2 * i] = __float_as_uint(f.x);
+            m[2 * i + 1] = __float_as_uint(f.y);
+        }
+    }
+}
+// The largest of all of them.
+template <typename T> __device__ __forceinline__ uint32_t top_of(const Top<T> &t) {
+    if constexpr (sizeof(T) == 4) {
+        uint32_t m = t.w[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) m = max(m, t.w[i]);
+        return m;
+    } else {
+        const uint32_t p = __vmaxu2(__vmaxu2(t.w[0], t.w[1]), __vmaxu2(t.w[2], t.w[3]));
+        return __float_as_uint(two_floats<T>(max(p & 0xffffu, p >> 16)).x);
     }
 }
 
@@ -140,15 +177,21 @@ quantize_rows_kernel(const T *__restrict__ x, int64_t x_stride, RowsArgs a) {
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float f[8];
-        floats_of(v[i], f);
-        uint32_t amax = 0;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) amax = max(amax, magnitude(f[u]));
+        Top<T> top;
+        raise(top, v[i]);
+        uint32_t amax = top_of(top);
 #pragma unroll
         for (int d = 1; d < kBlock / 8; d <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, d));
         const uint32_t byte = scale_byte(amax, fexp);
-        const uint2 q = eight_bits(f, byte, a.e5m2);
+        uint2 q = make_uint2(kNanBytes, kNanBytes);
+        if (byte != 255u) {
+            const float s = inverse_scale(byte);
+            float f[8];
+            floats_of(v[i], f);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) f[u] *= s;
+            q = eight_bytes(f, a.e5m2);
+        }
         const int64_t t = r0 + i;
         if (t < a.in_rows && c < a.cols) {
             const bool scaler = lane % (kBlock / 8) == 0;
@@ -197,9 +240,9 @@ struct TileArgs {
 };
 
 template <typename T, bool kWide, bool kSquare>
-__global__ void __launch_bounds__(kQThreads)
+__global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 4 : 2)
 quantize_tiles_kernel(const T *__restrict__ x, TileArgs a) {
-    __shared__ uint32_t top[16][128];
+    __shared__ alignas(16) uint32_t top[16][128];
     __shared__ uint32_t bytes[128];
     __shared__ GroupTable table;
     grid_dependency_wait();
@@ -240,21 +283,12 @@ quantize_tiles_kernel(const T *__restrict__ x, TileArgs a) {
             const int r = ty + 16 * i;
             v[i] = r < valid ? load8<T, kWide>(src + r * a.x_stride, c, a.cols) : no_eight<T>();
         }
+        Top<T> mine;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) raise(mine, v[i]);
         uint32_t m[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) m[u] = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float f[8];
-            floats_of(v[i], f);
-#pragma unroll
-            for (int u = 0; u < 8; ++u) m[u] = max(m[u], magnitude(f[u]));
-        }
         if (kSquare) {
-            uint32_t all = 0;
-#pragma unroll
-            for (int u = 0; u < 8; ++u) all = max(all, m[u]);
-            all = __reduce_max_sync(0xffffffffu, all);
+            uint32_t all = __reduce_max_sync(0xffffffffu, top_of(mine));
             if (lane == 0) top[0][w] = all;
             __syncthreads();
             all = top[0][0];
@@ -265,8 +299,10 @@ quantize_tiles_kernel(const T *__restrict__ x, TileArgs a) {
 #pragma unroll
             for (int u = 0; u < 8; ++u) m[u] = byte;
         } else {
+            columns_of(mine, m);
 #pragma unroll
-            for (int u = 0; u < 8; ++u) top[ty][tx * 8 + u] = m[u];
+            for (int u = 0; u < 8; u += 4)
+                *reinterpret_cast<uint4 *>(&top[ty][tx * 8 + u]) = make_uint4(m[u], m[u + 1], m[u + 2], m[u + 3]);
             __syncthreads();
             if (tid < 128) {
                 uint32_t all = 0;
@@ -294,12 +330,10 @@ quantize_tiles_kernel(const T *__restrict__ x, TileArgs a) {
             floats_of(v[i], f);
 #pragma unroll
             for (int u = 0; u < 8; ++u) f[u] *= s[u];
-            uint2 q;
-            q.x = two_eight_bit(f[0], f[1], a.e5m2) | two_eight_bit(f[2], f[3], a.e5m2) << 16;
-            q.y = two_eight_bit(f[4], f[5], a.e5m2) | two_eight_bit(f[6], f[7], a.e5m2) << 16;
+            uint2 q = eight_bytes(f, a.e5m2);
             if (r < valid) {
-                q.x = (q.x & ~nan[0]) | (0x7f7f7f7fu & nan[0]);
-                q.y = (q.y & ~nan[1]) | (0x7f7f7f7fu & nan[1]);
+                q.x = (q.x & ~nan[0]) | (kNanBytes & nan[0]);
+                q.y = (q.y & ~nan[1]) | (kNanBytes & nan[1]);
             }
             if (r < dst_rows) store8<kWide>(dst + r * a.q_stride, c, a.cols, q);
         }
