@@ -99,53 +99,82 @@ struct Tile {
     int32_t scale_row;                    // scales of 32: the 128-row tile of a's scales
 };
 
+// The group table in a warp's registers: lane l holds groups l and l + 32.  A
+// role looks a tile up between two tiles, where the tensor cores wait for it, so
+// the search is two ballots and not six dependent loads, and no division is a
+// full one.
+struct Groups {
+    int first0, first1;   // tiles of rows before the group
+    int begin0, begin1, size0, size1, pstart0, pstart1;
+    __device__ __forceinline__ Groups(const GroupTable &t, int lane)
+        : first0(t.istart[lane]), first1(t.istart[lane + 32]), begin0(t.begin[lane]), begin1(t.begin[lane + 32]),
+          size0(t.size[lane]), size1(t.size[lane + 32]), pstart0(t.pstart[lane]), pstart1(t.pstart[lane + 32]) {}
+    // the group of tile v of rows: the last one that starts at or before it
+    __device__ __forceinline__ int find(int v) const {
+        return __popc(__ballot_sync(0xffffffffu, first0 <= v)) + __popc(__ballot_sync(0xffffffffu, first1 <= v)) - 1;
+    }
+    __device__ __forceinline__ static int of(int lo, int hi, int g) {
+        return __shfl_sync(0xffffffffu, g < 32 ? lo : hi, g & 31);
+    }
+};
+
+// n / d for n >= 0, d > 0: a rounded quotient is at most one off below 2^22.
+__device__ __forceinline__ int quotient(int n, int d) {
+    if (n >= 1 << 22) return n / d;
+    int q = (int)__fdividef((float)n, (float)d);
+    const int r = n - q * d;
+    return r < 0 ? q - 1 : r >= d ? q + 1 : q;
+}
+
 // Tiles of a group go in strips of kStrip tiles of columns, row by row within
 // a strip, so that the tiles in flight share both operands in L2.  CTAs take
 // tiles in turn; where the last column of tiles is narrow (n_first of n_tiles
 // go first), those of all groups go last, which evens the CTAs' shares out.
 template <int kForm, int kN, int kTileRows>
-__device__ __forceinline__ Tile tile_at(const GroupTable &table, const MatArgs &a, int t, int rank) {
+__device__ __forceinline__ Tile tile_at(const Groups &groups, int row_tiles, const MatArgs &a, int t, int rank) {
     Tile o;
     int mt, nt;
-    if (kForm != kFormOuter && t >= table.istart[kMaxGroups] * a.n_first) {
-        t -= table.istart[kMaxGroups] * a.n_first;
-        o.g = find_group(table, kMaxGroups, t);
-        mt = t - table.istart[o.g];
+    if (kForm != kFormOuter && t >= row_tiles * a.n_first) {
+        t -= row_tiles * a.n_first;
+        o.g = groups.find(t);
+        mt = t - Groups::of(groups.first0, groups.first1, o.g);
         nt = a.n_first;
     } else {
         int local, m_tiles, n_tiles;
         if (kForm == kFormOuter) {
             m_tiles = a.m_tiles;
             n_tiles = a.n_tiles;
-            o.g = t / (m_tiles * n_tiles);
+            o.g = quotient(t, m_tiles * n_tiles);
             local = t - o.g * (m_tiles * n_tiles);
         } else {
             n_tiles = a.n_first;
-            o.g = find_group(table, kMaxGroups, t / n_tiles);
-            local = t - table.istart[o.g] * n_tiles;
-            m_tiles = table.istart[o.g + 1] - table.istart[o.g];
+            o.g = groups.find(quotient(t, n_tiles));
+            const int before = Groups::of(groups.first0, groups.first1, o.g);
+            local = t - before * n_tiles;
+            m_tiles = (Groups::of(groups.size0, groups.size1, o.g) + kTileRows - 1) / kTileRows;
         }
-        const int strip = local / (m_tiles * kStrip);
+        const int strip = quotient(local, m_tiles * kStrip);
         local -= strip * m_tiles * kStrip;
         const int width = min(kStrip, n_tiles - strip * kStrip);
-        mt = local / width;
+        mt = quotient(local, width);
         nt = strip * kStrip + local - mt * width;
     }
     const int row = mt * kTileRows + rank * 128;
+    const int size = Groups::of(groups.size0, groups.size1, o.g), pstart = Groups::of(groups.pstart0, groups.pstart1, o.g);
     o.n0 = nt * kN;
     o.n = min(kN, (a.N - o.n0 + 31) & ~31);
     if (kForm == kFormOuter) {
         o.row0 = row;
         o.rows = min(128, a.M - row);
-        o.k_base = table.pstart[o.g];
-        o.k_tiles = (table.size[o.g] + kTileK - 1) / kTileK;
+        o.k_base = pstart;
+        o.k_tiles = (size + kTileK - 1) / kTileK;
         o.scale_row = 0;
     } else {
-        o.row0 = table.begin[o.g] + row;
-        o.rows = min(128, table.size[o.g] - row);
+        o.row0 = Groups::of(groups.begin0, groups.begin1, o.g) + row;
+        o.rows = min(128, size - row);
         o.k_base = 0;
         o.k_tiles = a.k_tiles;
-        o.scale_row = (table.pstart[o.g] + row) / 128;
+        o.scale_row = (pstart + row) / 128;
     }
     return o;   // rows may be 0 or less in the second CTA of a pair
 }
@@ -256,13 +285,15 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
     if (kPair) cluster_sync();   // the barriers are there before the other CTA arrives on them
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    const int total = kForm == kFormOuter ? a.G * a.m_tiles * a.n_tiles : sh.table.istart[kMaxGroups] * a.n_tiles;
+    const Groups groups(sh.table, lane);
+    const int row_tiles = sh.table.istart[kMaxGroups];
+    const int total = kForm == kFormOuter ? a.G * a.m_tiles * a.n_tiles : row_tiles * a.n_tiles;
 
     if (w == 0) {
         uint32_t it = 0;
         bool ok = true;
         for (int t = first; ok && t < total; t += step) {
-            const Tile o = tile_at<kForm, kN, kTileRows>(sh.table, a, t, rank);
+            const Tile o = tile_at<kForm, kN, kTileRows>(groups, row_tiles, a, t, rank);
             const int n0 = o.n0 + (kPair ? rank * (o.n / 2) : 0);
             const int panels = (o.n + 127) / 128;   // of scales of 32
             const int sb0 = (o.g * ((a.N + 127) / 128) + o.n0 / 128) * a.k_tiles;
@@ -310,7 +341,7 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
         const uint64_t desc_b = smem_desc(p0 + kPanelBytes, kOuterB ? kPanelBytes : 16, 1024, 2);
         const uint64_t desc_s = smem_desc(s0, 128, 128, 0);
         for (int t = first; ok && t < total; t += step) {
-            const Tile o = tile_at<kForm, kN, kTileRows>(sh.table, a, t, 0);
+            const Tile o = tile_at<kForm, kN, kTileRows>(groups, row_tiles, a, t, 0);
             if (o.k_tiles == 0) continue;
             const uint32_t idesc = a.idesc | (uint32_t)(o.n / 8) << 17 | (uint32_t)(kTileRows / 16) << 24;
             ok = __all_sync(0xffffffffu, wait_or_abort(&sh.acc_empty, (n & 1) ^ 1, &sh.abort));
@@ -357,7 +388,7 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
         const uint32_t half = w & 1;
         bool ok = kScales == kScales128;
         for (int t = first; ok && t < total; t += step) {
-            const Tile o = tile_at<kForm, kN, kTileRows>(sh.table, a, t, rank);
+            const Tile o = tile_at<kForm, kN, kTileRows>(groups, row_tiles, a, t, rank);
             const int slots = (o.k_tiles + kScaleSteps - 1) / kScaleSteps;
             constexpr bool kRowsB = kForm == kFormOuter;
             const int b0 = o.k_base / kTileK;
@@ -406,7 +437,7 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
         uint32_t n = 0;
         bool ok = true;
         for (int t = first; ok && t < total; t += step) {
-            const Tile o = tile_at<kForm, kN, kTileRows>(sh.table, a, t, rank);
+            const Tile o = tile_at<kForm, kN, kTileRows>(groups, row_tiles, a, t, rank);
             uint32_t v[kCols];
             if (o.k_tiles > 0) {
                 ok = wait_or_abort(&sh.acc_full, n & 1, &sh.abort);
