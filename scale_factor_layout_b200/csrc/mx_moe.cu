@@ -28,8 +28,8 @@ namespace {
 // launches, because a CTA needs the counts of all earlier ones.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int64_t kSortOneCta = 8192;
-constexpr int64_t kSortChunk = 2048;   // slots of a CTA, at least
+constexpr int64_t kSortOneCta = 2048;
+constexpr int64_t kSortChunk = 1024;   // slots of a CTA, at least
 constexpr int kSortMaxCtas = 148;
 
 template <typename Id>

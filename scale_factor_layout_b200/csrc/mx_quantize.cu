@@ -155,11 +155,12 @@ struct RowsArgs {
     const int *last_end;
     int64_t in_rows, out_rows;
     int32_t cols, k, segments;
+    int32_t per_warp;                 // rows of a warp, 1 to 4
     bool e5m2;
 };
 
-// A CTA takes 32 rows x 256 columns, each warp 4 of the rows (4 loads in
-// flight a lane).  kOrder: row t is written to the rows row_of_slot[t, :], so a
+// A CTA takes 256 columns of 8 to 32 rows, a warp 1 to 4 of them: 4 loads in
+// flight a lane, or fewer where there are too few rows to fill the SMs.  kOrder: row t is written to the rows row_of_slot[t, :], so a
 // token is read and rounded once however many experts it goes to.
 template <typename T, bool kWide, int kBlock, bool kOrder>
 __global__ void __launch_bounds__(kQThreads)
@@ -168,15 +169,16 @@ quantize_rows_kernel(const T *__restrict__ x, int64_t x_stride, RowsArgs a) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int64_t band = blockIdx.x / a.segments;
     const int c = (int)(blockIdx.x - band * a.segments) * 256 + lane * 8;
-    const int64_t r0 = band * 32 + w * 4;
+    const int64_t r0 = (band * 8 + w) * a.per_warp;
     const int fexp = a.e5m2 ? 15 : 8;
     Eight<T> v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        v[i] = r0 + i < a.in_rows ? load8<T, kWide>(x + (r0 + i) * x_stride, c, a.cols) : no_eight<T>();
+        v[i] = i < a.per_warp && r0 + i < a.in_rows ? load8<T, kWide>(x + (r0 + i) * x_stride, c, a.cols) : no_eight<T>();
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+        if (i >= a.per_warp) break;
         Top<T> top;
         raise(top, v[i]);
         uint32_t amax = top_of(top);
@@ -415,10 +417,12 @@ mx_status mx_quantize_rows(const void *x, mx_dtype dtype, int64_t rows, int64_t 
     a.k = choices;
     a.segments = (int32_t)mx::div_up(cols, 256);
     a.e5m2 = out_dtype == MX_E5M2;
-    const int64_t grid = mx::div_up(rows, 32) * a.segments;
-    if (grid > INT_MAX) return MX_ERR_UNSUPPORTED;
     int sms = 0;
     if (mx_status st = mx_device_sms(&sms); st != MX_OK) return st;
+    a.per_warp = 4;
+    while (a.per_warp > 1 && mx::div_up(rows, 8 * a.per_warp) * a.segments < 2 * sms) a.per_warp /= 2;
+    const int64_t grid = mx::div_up(rows, 8 * a.per_warp) * a.segments;
+    if (grid > INT_MAX) return MX_ERR_UNSUPPORTED;
     const bool wide = mx::wide_ok(x, x_stride, 0, es, q, q_stride, 0, cols);
 #define MX_ROWS(T) (wide ? mx::rows_typed<T, true>(x, x_stride, a, block, grid, stream) : mx::rows_typed<T, false>(x, x_stride, a, block, grid, stream))
     if (dtype == MX_F32) return MX_ROWS(float);

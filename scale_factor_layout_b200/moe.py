@@ -26,6 +26,7 @@ torch and may be captured in a CUDA graph (after one call on the device).
 """
 from __future__ import annotations
 
+import functools
 from typing import NamedTuple
 
 import torch
@@ -117,6 +118,11 @@ def _check_out(out: torch.Tensor, shape, dtypes) -> None:
                          "dense along columns")
 
 
+@functools.lru_cache(maxsize=1024)
+def _sort_workspace(tokens: int, choices: int) -> int:
+    return B.mx_expert_sort_workspace(tokens, choices)
+
+
 def expert_sort(expert_ids: torch.Tensor, num_experts: int) -> ExpertOrder:
     """Sort the slots of ``expert_ids`` (int32 or int64 [tokens, choices]) by
     expert, stable; ids outside [0, num_experts) get no row."""
@@ -128,14 +134,14 @@ def expert_sort(expert_ids: torch.Tensor, num_experts: int) -> ExpertOrder:
     T, k = expert_ids.shape
     if k < 1:
         raise ValueError("expert_ids must have at least one choice a token")
-    dev = expert_ids.device
-    ends = torch.empty(num_experts, dtype=torch.int32, device=dev)
-    row_of_slot = torch.empty((T, k), dtype=torch.int32, device=dev)
-    slot_of_row = torch.empty(T * k, dtype=torch.int32, device=dev)
-    need = B.mx_expert_sort_workspace(T, k)
-    workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    _call("mx_expert_sort", dev, expert_ids.data_ptr(), 4 if expert_ids.dtype == torch.int32 else 8, T, k, num_experts,
-          ends.data_ptr(), row_of_slot.data_ptr(), slot_of_row.data_ptr(), workspace.data_ptr() if need else 0)
+    dev, i32, S = expert_ids.device, torch.int32, T * k
+    ends = torch.empty_strided((num_experts,), (1,), dtype=i32, device=dev)
+    row_of_slot = torch.empty_strided((T, k), (k, 1), dtype=i32, device=dev)
+    slot_of_row = torch.empty_strided((S,), (1,), dtype=i32, device=dev)
+    need = _sort_workspace(T, k)
+    workspace = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=dev).data_ptr() if need else 0
+    _call("mx_expert_sort", dev, expert_ids.data_ptr(), 4 if expert_ids.dtype == i32 else 8, T, k, num_experts,
+          ends.data_ptr(), row_of_slot.data_ptr(), slot_of_row.data_ptr(), workspace)
     return ExpertOrder(ends, row_of_slot, slot_of_row)
 
 
@@ -143,7 +149,7 @@ def expert_sort(expert_ids: torch.Tensor, num_experts: int) -> ExpertOrder:
 def _dispatch(x, order, out=None):
     T, k = order.row_of_slot.shape
     if out is None:
-        out = torch.empty((T * k, x.shape[1]), dtype=x.dtype, device=x.device)
+        out = x.new_empty(T * k, x.shape[1])
     _call("mx_dispatch_rows", x.device, x.data_ptr(), FLOATS[x.dtype], T, x.shape[1], _row_stride(x),
           order.row_of_slot.data_ptr(), k, order.group_ends.data_ptr(), order.group_ends.numel(), out.data_ptr(),
           _row_stride(out))
@@ -153,7 +159,7 @@ def _dispatch(x, order, out=None):
 def _combine(rows, order, weights, out=None):
     T, k = order.row_of_slot.shape
     if out is None:
-        out = torch.empty((T, rows.shape[1]), dtype=rows.dtype, device=rows.device)
+        out = rows.new_empty(T, rows.shape[1])
     _call("mx_combine_rows", rows.device, rows.data_ptr(), FLOATS[rows.dtype], T, rows.shape[1], _row_stride(rows),
           order.row_of_slot.data_ptr(), k, 0 if weights is None else weights.data_ptr(), out.data_ptr(),
           _row_stride(out))
@@ -248,7 +254,7 @@ def combine_rows_backward(grad: torch.Tensor, rows: torch.Tensor, order: ExpertO
     T, k = order.row_of_slot.shape
     if grad.dtype != rows.dtype or tuple(grad.shape) != (T, rows.shape[1]):
         raise ValueError(f"grad must be a {rows.dtype} tensor of shape ({T}, {rows.shape[1]})")
-    d_rows = torch.empty((T * k, rows.shape[1]), dtype=rows.dtype, device=rows.device)
+    d_rows = rows.new_empty(T * k, rows.shape[1])
     if rows.shape[1] == 0:
         return d_rows, torch.zeros_like(weights)
     d_weights = torch.empty_like(weights)
@@ -262,8 +268,9 @@ def combine_rows_backward(grad: torch.Tensor, rows: torch.Tensor, order: ExpertO
 # ------------------------------------------------------------------ quantization
 def _eight_bit_rows(shape, dtype, device) -> torch.Tensor:
     """8-bit rows that start on 16-byte boundaries, as the product reads them."""
-    q = torch.empty((*shape[:-1], _up(shape[-1], 16)), dtype=dtype, device=device)
-    return q if q.shape[-1] == shape[-1] else q[..., :shape[-1]]
+    stride = _up(shape[-1], 16)
+    strides = (stride, 1) if len(shape) == 2 else (shape[1] * stride, stride, 1)
+    return torch.empty_strided(shape, strides, dtype=dtype, device=device)
 
 
 def _check_eight_bit(dtype) -> None:
@@ -297,11 +304,11 @@ def quantize_rows(x: torch.Tensor, block: int = 128, dtype: torch.dtype = torch.
     q = _eight_bit_rows((out_rows, cols), dtype, x.device)
     blocks = _up(cols, block) // block
     if block == 128:
-        scales = torch.empty((blocks, out_rows), dtype=torch.uint8, device=x.device).t()
+        row_stride, block_stride = 1, out_rows
     else:
-        scales = torch.empty((out_rows, blocks), dtype=torch.uint8, device=x.device)
+        row_stride, block_stride = blocks, 1
+    scales = torch.empty_strided((out_rows, blocks), (row_stride, block_stride), dtype=torch.uint8, device=x.device)
     if out_rows and cols:
-        row_stride, block_stride = (1, out_rows) if block == 128 else (blocks, 1)
         _call("mx_quantize_rows", x.device, x.data_ptr(), FLOATS[x.dtype], rows, cols, _row_stride(x), block,
               EIGHT_BIT[dtype], slots, k, ends, G, q.data_ptr(), _row_stride(q, 16), scales.data_ptr(), row_stride,
               block_stride)
@@ -317,7 +324,7 @@ def quantize_cols(x: torch.Tensor, group_ends: torch.Tensor, dtype: torch.dtype 
     _check_ends("group_ends", group_ends)
     _check_cuda(x=x, group_ends=group_ends)
     rows, cols = x.shape
-    padded = B.mx_padded_rows(rows, group_ends.numel())
+    padded = _up(rows, 128) + 128 * group_ends.numel()   # mx_padded_rows
     q = _eight_bit_rows((padded, cols), dtype, x.device)
     scales = torch.empty((padded // 128, cols), dtype=torch.uint8, device=x.device)
     if cols:
@@ -403,7 +410,7 @@ def grouped_matmul(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_s
             if not s.is_contiguous() or s.numel() < need:
                 raise ValueError(f"{name} must be a contiguous blocked buffer of at least {need} bytes")
     if out is None:
-        out = torch.empty((rows, n), dtype=out_dtype, device=a.device)
+        out = torch.empty_strided((rows, n), (n, 1), dtype=out_dtype, device=a.device)
     else:
         _check_out(out, (rows, n), (out_dtype,))
     _call("mx_grouped_matmul_m", a.device, a.data_ptr(), EIGHT_BIT[a.dtype], _row_stride(a, 16), a_scales.data_ptr(),
@@ -436,7 +443,7 @@ def grouped_matmul_k(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b
         if cols > 1 and s.stride(1) != 1:
             raise ValueError(f"{name} must be dense along columns (stride(1) == 1)")
     if out is None:
-        out = torch.empty((G, m, n), dtype=out_dtype, device=a.device)
+        out = torch.empty_strided((G, m, n), (m * n, n, 1), dtype=out_dtype, device=a.device)
     else:
         _check_out(out, (G, m, n), (out_dtype,))
     _call("mx_grouped_matmul_k", a.device, a.data_ptr(), EIGHT_BIT[a.dtype], _row_stride(a, 16), a_scales.data_ptr(),
