@@ -53,6 +53,7 @@ constexpr int kOutRow = 64, kOutBytes = 32 * kOutRow;   // bytes of a row, and o
 constexpr int kPanelBytes = 128 * kTileK;   // 128 rows (or columns) of an operand in a stage
 constexpr int kTmemColumns = 512;
 constexpr int kScaleColumn = 480;           // 2 sets of 4 + 8 columns of scales
+constexpr int kTileSlots = 4;
 constexpr int kStrip = 8;                   // tiles of a strip of columns
 
 struct MatArgs {
@@ -67,7 +68,6 @@ struct MatArgs {
     int32_t n_tiles, m_tiles, k_tiles;      // m_tiles: contraction groups only
     int32_t out_type;                       // 0 f32, 1 bf16, 2 f16
     uint32_t idesc;
-    int32_t n_first;                        // row groups: tiles of columns that go first, see tile_at
     bool tma_out;                           // out's rows start on 16-byte boundaries
 };
 
@@ -89,6 +89,9 @@ struct Shared {
     GroupTable table;
     alignas(8) uint64_t full[kStages], empty[kStages], scale_full[kScaleSlots], scale_empty[kScaleSlots];
     alignas(8) uint64_t acc_full, acc_empty, drain;
+    alignas(16) uint4 answer;   // about a cancelled launch
+    alignas(8) uint64_t answered, tile_full[kTileSlots], tile_empty[kTileSlots];
+    int tiles[kTileSlots];
     uint32_t tmem;
     volatile int abort;
 };
@@ -116,6 +119,7 @@ struct Groups {
     __device__ __forceinline__ static int of(int lo, int hi, int g) {
         return __shfl_sync(0xffffffffu, g < 32 ? lo : hi, g & 31);
     }
+    __device__ __forceinline__ int last_end() const { return __shfl_sync(0xffffffffu, begin1 + size1, 31); }
 };
 
 // n / d for n >= 0, d > 0: a rounded quotient is at most one off below 2^22.
@@ -127,38 +131,37 @@ __device__ __forceinline__ int quotient(int n, int d) {
 }
 
 // Tiles of a group go in strips of kStrip tiles of columns, row by row within
-// a strip, so that the tiles in flight share both operands in L2.  CTAs take
-// tiles in turn; where the last column of tiles is narrow (n_first of n_tiles
-// go first), those of all groups go last, which evens the CTAs' shares out.
+// a strip, so that the tiles in flight share both operands in L2.  Behind the
+// groups' tiles come those of the rows behind the last group, which have no
+// contraction and are written as zeros.
 template <int kForm, int kN, int kTileRows>
 __device__ __forceinline__ Tile tile_at(const Groups &groups, int row_tiles, const MatArgs &a, int t, int rank) {
     Tile o;
-    int mt, nt;
-    if (kForm != kFormOuter && t >= row_tiles * a.n_first) {
-        t -= row_tiles * a.n_first;
-        o.g = groups.find(t);
-        mt = t - Groups::of(groups.first0, groups.first1, o.g);
-        nt = a.n_first;
-    } else {
-        int local, m_tiles, n_tiles;
-        if (kForm == kFormOuter) {
-            m_tiles = a.m_tiles;
-            n_tiles = a.n_tiles;
-            o.g = quotient(t, m_tiles * n_tiles);
-            local = t - o.g * (m_tiles * n_tiles);
-        } else {
-            n_tiles = a.n_first;
-            o.g = groups.find(quotient(t, n_tiles));
-            const int before = Groups::of(groups.first0, groups.first1, o.g);
-            local = t - before * n_tiles;
-            m_tiles = (Groups::of(groups.size0, groups.size1, o.g) + kTileRows - 1) / kTileRows;
-        }
-        const int strip = quotient(local, m_tiles * kStrip);
-        local -= strip * m_tiles * kStrip;
-        const int width = min(kStrip, n_tiles - strip * kStrip);
-        mt = quotient(local, width);
-        nt = strip * kStrip + local - mt * width;
+    if (kForm != kFormOuter && t >= row_tiles * a.n_tiles) {
+        t -= row_tiles * a.n_tiles;
+        const int mt = quotient(t, a.n_tiles);
+        o.g = 0;
+        o.row0 = groups.last_end() + mt * kTileRows + rank * 128;
+        o.rows = min(128, a.rows - o.row0);
+        o.n0 = (t - mt * a.n_tiles) * kN;
+        o.n = kN;
+        o.k_base = o.k_tiles = o.scale_row = 0;
+        return o;
     }
+    int local, m_tiles;
+    if (kForm == kFormOuter) {
+        m_tiles = a.m_tiles;
+        o.g = quotient(t, m_tiles * a.n_tiles);
+        local = t - o.g * (m_tiles * a.n_tiles);
+    } else {
+        o.g = groups.find(quotient(t, a.n_tiles));
+        local = t - Groups::of(groups.first0, groups.first1, o.g) * a.n_tiles;
+        m_tiles = (Groups::of(groups.size0, groups.size1, o.g) + kTileRows - 1) / kTileRows;
+    }
+    const int strip = quotient(local, m_tiles * kStrip);
+    local -= strip * m_tiles * kStrip;
+    const int width = min(kStrip, a.n_tiles - strip * kStrip);
+    const int mt = quotient(local, width), nt = strip * kStrip + local - mt * width;
     const int row = mt * kTileRows + rank * 128;
     const int size = Groups::of(groups.size0, groups.size1, o.g), pstart = Groups::of(groups.pstart0, groups.pstart1, o.g);
     o.n0 = nt * kN;
@@ -244,6 +247,59 @@ __device__ __forceinline__ void stage_row(uint8_t *box, const uint32_t *v, int l
     }
 }
 
+// The tiles of a CTA (of a pair).  The first is its own block's; for each that it
+// begins, the producer of rank 0 cancels the launch of a block that has not
+// started, takes over its tile and tells every warp.  So faster SMs do more
+// tiles, which the clocks and distances to memory of 148 SMs, groups' uneven
+// ends and narrow last columns of tiles all ask for.
+template <typename Sh, bool kPair>
+struct TileStream {
+    Sh &sh;
+    uint32_t n = 0;
+    int tile;
+    __device__ __forceinline__ TileStream(Sh &s, int first) : sh(s), tile(first) {}
+    // For the warps that are told: the next tile; false after the last.
+    __device__ __forceinline__ bool next(int lane) {
+        const uint32_t slot = n % kTileSlots;
+        const bool ok = wait_or_abort(&sh.tile_full[slot], n / kTileSlots & 1, &sh.abort);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        tile = *reinterpret_cast<volatile int *>(&sh.tiles[slot]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(leader_addr<kPair>(&sh.tile_empty[slot]));
+        ++n;
+        return tile >= 0;
+    }
+    // For the producer of rank 0: ask for a tile, and take and announce it.
+    __device__ __forceinline__ void ask() {
+        if (elect_one()) {
+            mbar_arrive_expect_tx(&sh.answered, 16);
+            cancel_launch(&sh.answer, &sh.answered);
+        }
+        __syncwarp();
+    }
+    __device__ __forceinline__ bool take() {
+        const uint32_t slot = n % kTileSlots;
+        bool ok = wait_or_abort(&sh.answered, n & 1, &sh.abort);
+        ok = ok && wait_or_abort(&sh.tile_empty[slot], (n / kTileSlots & 1) ^ 1, &sh.abort);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        tile = cancelled_block(&sh.answer);
+        if (tile >= 0) tile /= kPair ? 2 : 1;
+        fence_proxy_async_smem();   // the answer is read before the next one is written
+        __syncwarp();
+        if (elect_one()) {
+#pragma unroll
+            for (int c = 0; c < (kPair ? 2 : 1); ++c) {
+                const uint32_t bar = addr_in<kPair>(&sh.tile_full[slot], c);
+                mbar_expect_at(bar, 4);
+                store_word_at(addr_in<kPair>(&sh.tiles[slot], c), (uint32_t)tile, bar);
+            }
+        }
+        __syncwarp();
+        ++n;
+        return tile >= 0;
+    }
+};
+
 template <int kForm, int kScales, int kN, bool kPair>
 __global__ void __launch_bounds__(kMatThreads, 1)
 grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
@@ -257,7 +313,6 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
     Sh &sh = *reinterpret_cast<Sh *>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int rank = kPair ? (int)cluster_rank() : 0;
-    const int first = blockIdx.x / kCtas, step = gridDim.x / kCtas;
 
     if (w == 0 && lane == 0) {
         tma_prefetch_desc(&maps.a);
@@ -273,6 +328,12 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
         mbar_init(&sh.acc_full, 1);
         mbar_init(&sh.acc_empty, kDrainWarps * kCtas);
         mbar_init(&sh.drain, 1);
+        mbar_init(&sh.answered, 1);
+        for (int i = 0; i < kTileSlots; ++i) {
+            mbar_init(&sh.tile_full[i], 1);
+            // the matrix warp, the scale warps, the draining warps, the other CTA's producer
+            mbar_init(&sh.tile_empty[i], 1 + (kScales == kScales128 ? 2 : 0) * kCtas + kDrainWarps * kCtas + (kCtas - 1));
+        }
         sh.abort = 0;
         fence_mbar_init();
     }
@@ -287,13 +348,18 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
     const uint32_t tmem = sh.tmem;
     const Groups groups(sh.table, lane);
     const int row_tiles = sh.table.istart[kMaxGroups];
-    const int total = kForm == kFormOuter ? a.G * a.m_tiles * a.n_tiles : row_tiles * a.n_tiles;
+    // tiles in all: the launch has an upper bound of blocks, the last of them without work
+    const int total = kForm == kFormOuter ? a.G * a.m_tiles * a.n_tiles
+                                          : (row_tiles + (a.rows - groups.last_end() + kTileRows - 1) / kTileRows) * a.n_tiles;
+    TileStream<Sh, kPair> tiles(sh, blockIdx.x / kCtas);
 
     if (w == 0) {
         uint32_t it = 0;
         bool ok = true;
-        for (int t = first; ok && t < total; t += step) {
-            const Tile o = tile_at<kForm, kN, kTileRows>(groups, row_tiles, a, t, rank);
+        do {
+            if (rank == 0) tiles.ask();
+            if (tiles.tile >= total) continue;
+            const Tile o = tile_at<kForm, kN, kTileRows>(groups, row_tiles, a, tiles.tile, rank);
             const int n0 = o.n0 + (kPair ? rank * (o.n / 2) : 0);
             const int panels = (o.n + 127) / 128;   // of scales of 32
             const int sb0 = (o.g * ((a.N + 127) / 128) + o.n0 / 128) * a.k_tiles;
@@ -326,8 +392,8 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
                 }
                 __syncwarp();
             }
-        }
-        if (!ok) {   // copies in flight, a few microseconds' worth, land before the CTA leaves
+        } while (ok && (rank == 0 ? tiles.take() : tiles.next(lane)));
+        if (sh.abort) {   // copies in flight, a few microseconds' worth, land before the CTA leaves
             const long long t0 = clock64();
             while (clock64() - t0 < (1ll << 22)) {}
         }
@@ -340,8 +406,9 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
         const uint64_t desc_a = smem_desc(p0, kOuterA ? kPanelBytes : 16, 1024, 2);
         const uint64_t desc_b = smem_desc(p0 + kPanelBytes, kOuterB ? kPanelBytes : 16, 1024, 2);
         const uint64_t desc_s = smem_desc(s0, 128, 128, 0);
-        for (int t = first; ok && t < total; t += step) {
-            const Tile o = tile_at<kForm, kN, kTileRows>(groups, row_tiles, a, t, 0);
+        if (ok) do {
+            if (tiles.tile >= total) continue;
+            const Tile o = tile_at<kForm, kN, kTileRows>(groups, row_tiles, a, tiles.tile, 0);
             if (o.k_tiles == 0) continue;
             const uint32_t idesc = a.idesc | (uint32_t)(o.n / 8) << 17 | (uint32_t)(kTileRows / 16) << 24;
             ok = __all_sync(0xffffffffu, wait_or_abort(&sh.acc_empty, (n & 1) ^ 1, &sh.abort));
@@ -377,8 +444,8 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
                 __syncwarp();
             }
             ++n;
-        }
-        if (!ok && rank == 0) {   // matrix instructions in flight end before the tensor memory is freed
+        } while (ok && tiles.next(lane));
+        if (sh.abort && rank == 0) {   // matrix instructions in flight end before the tensor memory is freed
             if (elect_one()) tc_commit<kPair>(&sh.drain);
             __syncwarp();
             mbar_wait_bounded(&sh.drain, 0, 1ll << 24);
@@ -387,8 +454,9 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
         uint32_t sc = 0;   // slots before this tile; a warp fills every other one
         const uint32_t half = w & 1;
         bool ok = kScales == kScales128;
-        for (int t = first; ok && t < total; t += step) {
-            const Tile o = tile_at<kForm, kN, kTileRows>(groups, row_tiles, a, t, rank);
+        if (ok) do {
+            if (tiles.tile >= total) continue;
+            const Tile o = tile_at<kForm, kN, kTileRows>(groups, row_tiles, a, tiles.tile, rank);
             const int slots = (o.k_tiles + kScaleSteps - 1) / kScaleSteps;
             constexpr bool kRowsB = kForm == kFormOuter;
             const int b0 = o.k_base / kTileK;
@@ -430,14 +498,15 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
                 if (lane == 0) mbar_arrive_at(leader_addr<kPair>(&sh.scale_full[s]));
             }
             sc += slots;
-        }
+        } while (ok && tiles.next(lane));
     } else {
         const int quarter = w & 3, part = (w - 4) >> 2;   // rows 32 * quarter.., columns part * kN / 2..
         constexpr int kCols = kN / 2;
         uint32_t n = 0;
         bool ok = true;
-        for (int t = first; ok && t < total; t += step) {
-            const Tile o = tile_at<kForm, kN, kTileRows>(groups, row_tiles, a, t, rank);
+        do {
+            if (tiles.tile >= total) continue;
+            const Tile o = tile_at<kForm, kN, kTileRows>(groups, row_tiles, a, tiles.tile, rank);
             uint32_t v[kCols];
             if (o.k_tiles > 0) {
                 ok = wait_or_abort(&sh.acc_full, n & 1, &sh.abort);
@@ -490,22 +559,8 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
                     else store_row<__half>(a.out, at + c, u, a.N - n0 - c);
                 }
             }
-        }
+        } while (ok && tiles.next(lane));
         if (lane == 0) bulk_wait_all();
-        if (kForm != kFormOuter) {   // rows behind the last group
-            const int es = a.out_type == 0 ? 4 : 2;
-            const int64_t bytes = (int64_t)a.N * es;
-            int64_t r = sh.table.begin[a.G - 1] + sh.table.size[a.G - 1] + (int64_t)blockIdx.x * kDrainWarps + (w - 4);
-            for (; r < a.rows; r += (int64_t)gridDim.x * kDrainWarps) {
-                uint8_t *row = static_cast<uint8_t *>(a.out) + r * a.out_stride * es;
-                int64_t i = 0;
-                if (a.tma_out) {
-                    i = bytes & ~int64_t(15);
-                    for (int64_t b = lane * 16; b < i; b += 512) *reinterpret_cast<uint4 *>(row + b) = make_uint4(0u, 0u, 0u, 0u);
-                }
-                for (i += lane * 2; i < bytes; i += 64) *reinterpret_cast<uint16_t *>(row + i) = 0;
-            }
-        }
     }
     __syncwarp();
     tc_fence_before();
@@ -525,45 +580,36 @@ mx_status launch_product(const Maps &maps, MatArgs a, cudaStream_t stream) {
     auto kernel = grouped_product<kForm, kScales, kN, kPair>;
     a.n_tiles = (int32_t)div_up(a.N, kN);
     a.m_tiles = (int32_t)div_up(a.M, Sh::kTileRows);
-    a.n_first = a.N % kN != 0 && a.N % kN <= kN / 2 ? a.n_tiles - 1 : a.n_tiles;
     // an upper bound on the tiles, known without the group ends
     const int64_t tiles = kForm == kFormOuter ? (int64_t)a.m_tiles * a.n_tiles * a.G
                                               : (div_up(a.rows, Sh::kTileRows) + a.G) * a.n_tiles;
     if (tiles > INT_MAX / 2) return MX_ERR_UNSUPPORTED;
 
     static std::mutex mu;
-    static int resident[kMatMaxDevices] = {};   // CTAs, or pairs, that run at once
+    static bool ready[kMatMaxDevices] = {};
     int dev = 0, sms = 0;
     if (mx_status st = mx_device_sms(&sms); st != MX_OK) return st;
     if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return mx_record_cuda_error(e);
     if (dev < 0 || dev >= kMatMaxDevices) return MX_ERR_UNSUPPORTED;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!ready[dev]) {
+            if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); e != cudaSuccess)
+                return mx_record_cuda_error(e);
+            ready[dev] = true;
+        }
+    }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = kCtas;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(tiles * kCtas));
     cfg.blockDim = dim3(kMatThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = kPair ? 1 : 0;
-    int most;
-    {
-        std::lock_guard<std::mutex> lock(mu);
-        if (resident[dev] == 0) {
-            if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); e != cudaSuccess)
-                return mx_record_cuda_error(e);
-            int n = sms;
-            if (kPair) {
-                cfg.gridDim = dim3(sms / 2 * 2);
-                if (cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg); e != cudaSuccess || n < 1)
-                    return mx_record_cuda_error(e != cudaSuccess ? e : cudaErrorInvalidConfiguration);
-            }
-            resident[dev] = n;
-        }
-        most = resident[dev];
-    }
-    cfg.gridDim = dim3((unsigned)((tiles < most ? tiles : most) * kCtas));
+    cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, maps, a);
     return e == cudaSuccess ? MX_OK : mx_record_cuda_error(e);
 }

@@ -72,6 +72,41 @@ __device__ __forceinline__ void mbar_expect_at(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
+// ------------------------------------------------------------------ work
+// Cancels the launch of a cluster that has not started and takes its place: 16
+// bytes about it arrive in shared memory, counted on `bar`.
+__device__ __forceinline__ void cancel_launch(uint4 *answer, uint64_t *bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                 ::"r"(smem_addr(answer)), "r"(smem_addr(bar)) : "memory");
+}
+// The first CTA of the cancelled cluster, or -1 if none was left.
+__device__ __forceinline__ int cancelled_block(const uint4 *answer) {
+    uint32_t x, ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %1, 1, 0, p;\n\t"
+        "mov.u32 %0, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, _, _, _}, r;\n\t}"
+        : "=r"(x), "=r"(ok) : "r"(smem_addr(answer)) : "memory");
+    return ok ? (int)x : -1;
+}
+// The address of this CTA's shared variable in the CTA of the given rank.
+template <bool kPair>
+__device__ __forceinline__ uint32_t addr_in(const void *p, uint32_t rank) {
+    const uint32_t here = smem_addr(p);
+    if (!kPair) return here;
+    uint32_t there;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(here), "r"(rank));
+    return there;
+}
+// A word into another CTA's shared memory, counted on a barrier there.
+__device__ __forceinline__ void store_word_at(uint32_t addr, uint32_t value, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];"
+                 ::"r"(addr), "r"(value), "r"(bar) : "memory");
+}
+
 // ------------------------------------------------------------------ tensor memory
 template <bool kPair>
 __device__ __forceinline__ void tmem_alloc(uint32_t *where, uint32_t columns) {
