@@ -264,8 +264,10 @@ struct TileStream {
         const bool ok = wait_or_abort(&sh.tile_full[slot], n / kTileSlots & 1, &sh.abort);
         if (!__all_sync(0xffffffffu, ok)) return false;
         tile = *reinterpret_cast<volatile int *>(&sh.tiles[slot]);
-        __syncwarp();
-        if (lane == 0) mbar_arrive_at(leader_addr<kPair>(&sh.tile_empty[slot]));
+        // The arrival lets the slot be overwritten, and must not overtake the load: behind a
+        // queue of stores that can take longer than the arrival and the next announcement.  The
+        // vote needs every lane's value (all are -1 or more), and the arrival needs the vote.
+        if (__all_sync(0xffffffffu, tile >= -1) && lane == 0) mbar_arrive_at(leader_addr<kPair>(&sh.tile_empty[slot]));
         ++n;
         return tile >= 0;
     }
@@ -495,7 +497,7 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_at(leader_addr<kPair>(&sh.scale_full[s]));
+                if (lane == 0) mbar_release_at(leader_addr<kPair>(&sh.scale_full[s]));
             }
             sc += slots;
         } while (ok && tiles.next(lane));

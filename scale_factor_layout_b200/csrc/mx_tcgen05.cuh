@@ -59,14 +59,19 @@ __device__ __forceinline__ uint32_t leader_addr(const void *p) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(there) : "r"(here));
     return there;
 }
-// Arrivals on a barrier of either CTA of the pair.  What they order is read by
-// the tensor cores and the copy engine, not by threads: scale bytes by a proxy
-// fence before the arrival, tensor memory by the tcgen05 fences, operand bytes
-// by the barrier's own count.  So the arrivals carry no cluster-wide release,
-// and the waits no cluster-wide acquire: on a B200 those took the 128 x 256
-// loop from about 1100 to 2000 clocks a stage.
+// Arrivals on a barrier of either CTA of the pair.  A release at cluster scope
+// waits for everything the thread has in flight, which the roles that pace the
+// loop cannot afford: with releases on every arrival and acquires on every wait
+// the 128 x 256 loop took about 2000 clocks a stage instead of 1100.  So only
+// what a thread wrote itself is released (the scale bytes); the others order
+// nothing that a thread still has under way: operand bytes are counted by the
+// barrier, tensor memory has been waited for, and a word that was read is in a
+// register, on which the arrival depends.
 __device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_release_at(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void mbar_expect_at(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
