@@ -226,11 +226,22 @@ __device__ __forceinline__ uint4 tile_line(const uint32_t (&b)[16]) {
 }
 
 template <typename T>
-__device__ __forceinline__ void store_row(void *out, int64_t at, const uint32_t (&v)[32], int valid) {
+__device__ __forceinline__ void store_row(void *out, int64_t at, const uint32_t *v, int valid, bool wide) {
     T *dst = static_cast<T *>(out) + at;
+    constexpr int N = 16 / sizeof(T);
+    if (wide && valid >= 32) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-        if (i < valid) dst[i] = from_f32<T>(__uint_as_float(v[i]));
+        for (int i = 0; i < 32; i += N) {
+            float f[N];
+#pragma unroll
+            for (int u = 0; u < N; ++u) f[u] = __uint_as_float(v[i + u]);
+            *reinterpret_cast<uint4 *>(dst + i) = pack<T, N>(f);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < valid) dst[i] = from_f32<T>(__uint_as_float(v[i]));
+    }
 }
 
 // 64 bytes of this lane's row into the warp's box of 32 rows, with the 64-byte
@@ -553,12 +564,10 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
                 const int64_t at = (kForm == kFormOuter ? o.g * a.out_group : 0) + (int64_t)(o.row0 + r0 + lane) * a.out_stride + n0;
 #pragma unroll
                 for (int c = 0; c < kCols; c += 32) {
-                    uint32_t u[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) u[i] = v[c + i];
-                    if (a.out_type == 0) store_row<float>(a.out, at + c, u, a.N - n0 - c);
-                    else if (a.out_type == 1) store_row<__nv_bfloat16>(a.out, at + c, u, a.N - n0 - c);
-                    else store_row<__half>(a.out, at + c, u, a.N - n0 - c);
+                    const int valid = a.N - n0 - c;
+                    if (a.out_type == 0) store_row<float>(a.out, at + c, v + c, valid, a.tma_out);
+                    else if (a.out_type == 1) store_row<__nv_bfloat16>(a.out, at + c, v + c, valid, a.tma_out);
+                    else store_row<__half>(a.out, at + c, v + c, valid, a.tma_out);
                 }
             }
         } while (ok && tiles.next(lane));
