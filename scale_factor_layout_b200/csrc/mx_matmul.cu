@@ -23,6 +23,10 @@
 // holds 128 rows of a and half of b's 256, so a stage brings 32 KB for the work
 // that takes 48 KB alone.  Shared memory bounds the loop (a stage is written
 // once and read once, 128 bytes a clock), so that is what a pair wins.
+// Where there are too few tiles for the SMs (few rows, few groups), tiles are
+// 128 x 128 and the contraction of one is split over a cluster of CTAs, which
+// add their parts up through each other's shared memory, in the order of the
+// parts.
 // Operands whose contraction is the outer dimension in memory (weights read
 // for the input gradient, both operands of the weight gradient) are loaded as
 // they are and read through descriptors of that order: nothing is transposed
@@ -313,9 +317,72 @@ struct TileStream {
     }
 };
 
-template <int kForm, int kScales, int kN, bool kPair>
+// The parts of a split tile, added up.  Each CTA of the cluster owns an equal
+// share of the tile's columns and gets the other parts' values of them in its
+// stages, which no load or matrix instruction uses any more once all have
+// emptied their accumulators (the first barrier); after the second it adds them
+// in the order of the parts and writes them out.
+template <int kForm, int kN>
+__device__ __forceinline__ void add_parts(uint8_t *stages, const Tile &o, const MatArgs &a, const uint32_t (&v)[kN / 2],
+                                          int part, int parts, int row, int half, int thread) {
+    const int share = kN / parts;   // columns of a CTA: 16 to 64
+    // [part][128][share], rows 4 words further apart: a warp writes 32 rows at once, 16 bytes of
+    // each, which a distance of 64, 128 or 256 bytes would put into the same banks
+    float *mine = reinterpret_cast<float *>(stages);
+    const int pitch = share + 4;
+    __syncwarp();
+    cluster_sync();
+    if (row < o.rows) {
+#pragma unroll
+        for (int c = 0; c < kN / 2; c += 4) {
+            const int col = half * (kN / 2) + c, owner = col / share;
+            float *at = mine + (part * 128 + row) * pitch + (col - owner * share);
+            if (owner == part) *reinterpret_cast<uint4 *>(at) = make_uint4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+            else asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};"
+                              ::"r"(addr_in<true>(at, owner)), "r"(v[c]), "r"(v[c + 1]), "r"(v[c + 2]), "r"(v[c + 3]) : "memory");
+        }
+    }
+    __syncwarp();
+    cluster_sync();
+    const int es = a.out_type == 0 ? 4 : 2;
+    for (int i = thread; i < 128 * share / 8; i += 32 * kDrainWarps) {   // eight columns of a row at a time
+        const int r = i / (share / 8), c0 = (i - r * (share / 8)) * 8, n = o.n0 + part * share + c0;
+        if (r >= o.rows || n >= a.N) continue;
+        float sum[8] = {};
+        for (int q = 0; q < parts; ++q) {
+            const float4 *src = reinterpret_cast<const float4 *>(mine + (q * 128 + r) * pitch + c0);
+            const float4 x = src[0], y = src[1];
+            sum[0] += x.x, sum[1] += x.y, sum[2] += x.z, sum[3] += x.w;
+            sum[4] += y.x, sum[5] += y.y, sum[6] += y.z, sum[7] += y.w;
+        }
+        const int64_t at = (kForm == kFormOuter ? o.g * a.out_group : 0) + (int64_t)(o.row0 + r) * a.out_stride + n;
+        if (a.tma_out && es == 2 && n + 8 <= a.N) {
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at) =
+                a.out_type == 1 ? pack<__nv_bfloat16, 8>(sum) : pack<__half, 8>(sum);
+        } else {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (n + u >= a.N) break;
+                if (a.out_type == 0) static_cast<float *>(a.out)[at + u] = sum[u];
+                else if (a.out_type == 1) static_cast<__nv_bfloat16 *>(a.out)[at + u] = from_f32<__nv_bfloat16>(sum[u]);
+                else static_cast<__half *>(a.out)[at + u] = from_f32<__half>(sum[u]);
+            }
+        }
+    }
+}
+
+// Steps of the contraction that part `part` of `parts` takes: whole slots of scales.
+__device__ __forceinline__ int split_begin(int k_tiles, int part, int parts) {
+    const int each = ((k_tiles + parts - 1) / parts + 3) & ~3;
+    return min(k_tiles, part * each);
+}
+
+enum Work { kAlone = 0, kPairs = 1, kSplits = 2 };   // a CTA, two CTAs, or a cluster of parts a tile
+
+template <int kForm, int kScales, int kN, int kWork>
 __global__ void __launch_bounds__(kMatThreads, 1)
 grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
+    constexpr bool kPair = kWork == kPairs, kSplit = kWork == kSplits;
     using Sh = Shared<kScales, kN, kPair>;
     constexpr int kScaleSlots = Sh::kScaleSlots;
     constexpr int kStages = Sh::kStages, kPanels = Sh::kPanels, kPanelsHere = Sh::kPanelsHere, kTileRows = Sh::kTileRows;
@@ -364,19 +431,23 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
     // tiles in all: the launch has an upper bound of blocks, the last of them without work
     const int total = kForm == kFormOuter ? a.G * a.m_tiles * a.n_tiles
                                           : (row_tiles + (a.rows - groups.last_end() + kTileRows - 1) / kTileRows) * a.n_tiles;
-    TileStream<Sh, kPair> tiles(sh, blockIdx.x / kCtas);
+    // a split tile is its cluster's only one
+    const int parts = kSplit ? (int)cluster_size() : 1, part = kSplit ? (int)cluster_rank() : 0;
+    TileStream<Sh, kPair> tiles(sh, blockIdx.x / (kSplit ? parts : kCtas));
 
     if (w == 0) {
         uint32_t it = 0;
         bool ok = true;
         do {
-            if (rank == 0) tiles.ask();
+            if (!kSplit && rank == 0) tiles.ask();
             if (tiles.tile >= total) continue;
             const Tile o = tile_at<kForm, kN, kTileRows>(groups, row_tiles, a, tiles.tile, rank);
+            const int k_begin = kSplit ? split_begin(o.k_tiles, part, parts) : 0;
+            const int k_end = kSplit ? split_begin(o.k_tiles, part + 1, parts) : o.k_tiles;
             const int n0 = o.n0 + (kPair ? rank * (o.n / 2) : 0);
             const int panels = (o.n + 127) / 128;   // of scales of 32
             const int sb0 = (o.g * ((a.N + 127) / 128) + o.n0 / 128) * a.k_tiles;
-            for (int k = 0; k < o.k_tiles; ++k, ++it) {
+            for (int k = k_begin; k < k_end; ++k, ++it) {
                 const uint32_t s = it % kStages, phase = it / kStages & 1;
                 ok = __all_sync(0xffffffffu, wait_or_abort(&sh.empty[s], phase ^ 1, &sh.abort));
                 if (!ok) break;
@@ -405,7 +476,7 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
                 }
                 __syncwarp();
             }
-        } while (ok && (rank == 0 ? tiles.take() : tiles.next(lane)));
+        } while (!kSplit && ok && (rank == 0 ? tiles.take() : tiles.next(lane)));
         if (sh.abort) {   // copies in flight, a few microseconds' worth, land before the CTA leaves
             const long long t0 = clock64();
             while (clock64() - t0 < (1ll << 22)) {}
@@ -422,12 +493,14 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
         if (ok) do {
             if (tiles.tile >= total) continue;
             const Tile o = tile_at<kForm, kN, kTileRows>(groups, row_tiles, a, tiles.tile, 0);
-            if (o.k_tiles == 0) continue;
+            const int k_begin = kSplit ? split_begin(o.k_tiles, part, parts) : 0;
+            const int k_end = kSplit ? split_begin(o.k_tiles, part + 1, parts) : o.k_tiles;
+            if (k_begin == k_end) continue;
             const uint32_t idesc = a.idesc | (uint32_t)(o.n / 8) << 17 | (uint32_t)(kTileRows / 16) << 24;
             ok = __all_sync(0xffffffffu, wait_or_abort(&sh.acc_empty, (n & 1) ^ 1, &sh.abort));
             if (!ok) break;
             tc_fence_after();
-            for (int k = 0; k < o.k_tiles; ++k, ++it) {
+            for (int k = k_begin; k < k_end; ++k, ++it) {
                 const uint32_t s = it % kStages, slot = sc % kScaleSlots;
                 const bool scales = k % kScaleSteps == 0;   // this stage brings new ones
                 if (kScales == kScales128 && scales)
@@ -450,14 +523,14 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         tc_mma_scaled<kPair>(tmem, da + q * (kOuterA ? 256 : 2), db + q * (kOuterB ? 256 : 2),
-                                             with_scale_byte(idesc, kScaleSteps == 4 ? k & 3 : q), ta, tb, k > 0 || q > 0);
+                                             with_scale_byte(idesc, kScaleSteps == 4 ? k & 3 : q), ta, tb, k > k_begin || q > 0);
                     tc_commit<kPair>(&sh.empty[s]);
-                    if (k == o.k_tiles - 1) tc_commit<kPair>(&sh.acc_full);
+                    if (k == k_end - 1) tc_commit<kPair>(&sh.acc_full);
                 }
                 __syncwarp();
             }
             ++n;
-        } while (ok && tiles.next(lane));
+        } while (!kSplit && ok && tiles.next(lane));
         if (sh.abort && rank == 0) {   // matrix instructions in flight end before the tensor memory is freed
             if (elect_one()) tc_commit<kPair>(&sh.drain);
             __syncwarp();
@@ -470,9 +543,11 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
         if (ok) do {
             if (tiles.tile >= total) continue;
             const Tile o = tile_at<kForm, kN, kTileRows>(groups, row_tiles, a, tiles.tile, rank);
-            const int slots = (o.k_tiles + kScaleSteps - 1) / kScaleSteps;
+            const int k_begin = kSplit ? split_begin(o.k_tiles, part, parts) : 0;
+            const int k_end = kSplit ? split_begin(o.k_tiles, part + 1, parts) : o.k_tiles;
+            const int slots = (k_end - k_begin + kScaleSteps - 1) / kScaleSteps;
             constexpr bool kRowsB = kForm == kFormOuter;
-            const int b0 = o.k_base / kTileK;
+            const int b0 = o.k_base / kTileK + k_begin;
             const int last = (kRowsB ? a.rows / kTileK : a.k_tiles) - 1;   // last step whose scales exist
             const LineSource sa(a.sa, a.sa_row, o.row0, kRowsB ? a.M : a.rows, lane);
             LineSource sb[kPanels];
@@ -492,7 +567,7 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
                         sb[p].load(bb[p], b0 + 4 * i, last, a.sb_block);
                     } else {
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) bb[p][u] = __ldg(sq[p] + min(4 * i + u, last) * a.sb_block);
+                        for (int u = 0; u < 4; ++u) bb[p][u] = __ldg(sq[p] + min(k_begin + 4 * i + u, last) * a.sb_block);
                     }
                 }
                 const uint32_t s = (sc + i) % kScaleSlots;
@@ -511,9 +586,9 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
                 if (lane == 0) mbar_release_at(leader_addr<kPair>(&sh.scale_full[s]));
             }
             sc += slots;
-        } while (ok && tiles.next(lane));
+        } while (!kSplit && ok && tiles.next(lane));
     } else {
-        const int quarter = w & 3, part = (w - 4) >> 2;   // rows 32 * quarter.., columns part * kN / 2..
+        const int quarter = w & 3, part_of_columns = (w - 4) >> 2;   // rows 32 * quarter.., columns part_of_columns * kN / 2..
         constexpr int kCols = kN / 2;
         uint32_t n = 0;
         bool ok = true;
@@ -521,7 +596,7 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
             if (tiles.tile >= total) continue;
             const Tile o = tile_at<kForm, kN, kTileRows>(groups, row_tiles, a, tiles.tile, rank);
             uint32_t v[kCols];
-            if (o.k_tiles > 0) {
+            if (kSplit ? split_begin(o.k_tiles, part, parts) < split_begin(o.k_tiles, part + 1, parts) : o.k_tiles > 0) {
                 ok = wait_or_abort(&sh.acc_full, n & 1, &sh.abort);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
@@ -529,17 +604,21 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
                 // all of it into registers, so that the next tile can begin
 #pragma unroll
                 for (int c = 0; c < kCols; c += 32)
-                    tc_load32(tmem + ((uint32_t)quarter << 21) + part * kCols + c, v + c);
+                    tc_load32(tmem + ((uint32_t)quarter << 21) + part_of_columns * kCols + c, v + c);
                 tc_wait_load();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_at(leader_addr<kPair>(&sh.acc_empty));
                 ++n;
-            } else {   // a group with no rows: its product is zero
+            } else {   // a group with no rows (or a part with no steps): its product is zero
 #pragma unroll
                 for (int i = 0; i < kCols; ++i) v[i] = 0;
             }
-            const int r0 = quarter * 32, n0 = o.n0 + part * kCols, es = a.out_type == 0 ? 4 : 2;
+            if (kSplit) {
+                add_parts<kForm, kN>(sh.operands[0], o, a, v, part, parts, quarter * 32 + lane, part_of_columns, tid - 128);
+                continue;
+            }
+            const int r0 = quarter * 32, n0 = o.n0 + part_of_columns * kCols, es = a.out_type == 0 ? 4 : 2;
             if (a.tma_out && r0 + 32 <= o.rows) {
                 // whole rows of the warp: through shared memory, since a lane holds a row and
                 // 32 rows a store instruction would be 32 separate lines
@@ -570,8 +649,18 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
                     else store_row<__half>(a.out, at + c, v + c, valid, a.tma_out);
                 }
             }
-        } while (ok && tiles.next(lane));
+        } while (!kSplit && ok && tiles.next(lane));
         if (lane == 0) bulk_wait_all();
+        if (kSplit && !(ok && tiles.tile < total)) {   // the barriers of add_parts, without a part
+            __syncwarp();
+            cluster_sync();
+            cluster_sync();
+        }
+    }
+    if (kSplit && w < 4) {
+        __syncwarp();
+        cluster_sync();
+        cluster_sync();
     }
     __syncwarp();
     tc_fence_before();
@@ -584,17 +673,25 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
 // ------------------------------------------------------------------ host side
 constexpr int kMatMaxDevices = 128;
 
-template <int kForm, int kScales, int kN, bool kPair>
-mx_status launch_product(const Maps &maps, MatArgs a, cudaStream_t stream) {
-    using Sh = Shared<kScales, kN, kPair>;
-    constexpr int smem = (int)sizeof(Sh) + 1024, kCtas = kPair ? 2 : 1;
-    auto kernel = grouped_product<kForm, kScales, kN, kPair>;
+// The most 128-row (or `tile`-row) tiles that groups of `rows` rows in all, and
+// the rows behind them, can make: each has a row at least.
+int64_t most_row_tiles(int64_t rows, int64_t groups, int64_t tile) {
+    const int64_t n = div_up(rows, tile) + groups;
+    return n < rows ? n : rows;
+}
+
+template <int kForm, int kScales, int kN, int kWork>
+mx_status launch_product(const Maps &maps, MatArgs a, int parts, cudaStream_t stream) {
+    using Sh = Shared<kScales, kN, kWork == kPairs>;
+    constexpr int smem = (int)sizeof(Sh) + 1024;
+    const int ctas = kWork == kPairs ? 2 : kWork == kSplits ? parts : 1;
+    auto kernel = grouped_product<kForm, kScales, kN, kWork>;
     a.n_tiles = (int32_t)div_up(a.N, kN);
     a.m_tiles = (int32_t)div_up(a.M, Sh::kTileRows);
     // an upper bound on the tiles, known without the group ends
     const int64_t tiles = kForm == kFormOuter ? (int64_t)a.m_tiles * a.n_tiles * a.G
-                                              : (div_up(a.rows, Sh::kTileRows) + a.G) * a.n_tiles;
-    if (tiles > INT_MAX / 2) return MX_ERR_UNSUPPORTED;
+                                              : most_row_tiles(a.rows, a.G, Sh::kTileRows) * a.n_tiles;
+    if (tiles > INT_MAX / 8) return MX_ERR_UNSUPPORTED;
 
     static std::mutex mu;
     static bool ready[kMatMaxDevices] = {};
@@ -613,9 +710,9 @@ mx_status launch_product(const Maps &maps, MatArgs a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kCtas;
+    attr[0].val.clusterDim.x = ctas;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3((unsigned)(tiles * kCtas));
+    cfg.gridDim = dim3((unsigned)(tiles * ctas));
     cfg.blockDim = dim3(kMatThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -653,8 +750,32 @@ mx_status out_map(CUtensorMap *map, const void *p, int64_t row_bytes, int64_t ro
 int out_code(mx_dtype t) { return t == MX_F32 ? 0 : t == MX_BF16 ? 1 : t == MX_F16 ? 2 : -1; }
 bool eight(mx_dtype t) { return t == MX_E4M3 || t == MX_E5M2; }
 
-bool use_pair(int64_t rows_of_group) {
-    return rows_of_group > 128;
+// How a product is spread over the SMs.  `row_tiles`: 128-row tiles if the groups
+// are even; `most`: the most that there can be; `rows`: rows of a group, on
+// average; `steps`: of the contraction.
+struct Plan { Work work; bool narrow; int parts; };
+Plan plan_of(int64_t row_tiles, int64_t most, int64_t n, int64_t rows, int64_t steps, int sms) {
+    // 128 x 128 tiles where they fit the SMs at once, and of their contraction as
+    // many parts as clusters of that size run at once on a B200 (74 of 2 CTAs, 33
+    // of 4, 15 of 8: clusters do not cross the borders of its processor groups)
+    const int64_t tiles = row_tiles * div_up(n, 128);
+    if (tiles <= sms) {
+        const int64_t clusters = most * div_up(n, 128);
+        int parts = 1;
+        if (steps >= 8 && clusters <= sms / 2) parts = 2;
+        if (steps >= 16 && clusters <= 33) parts = 4;
+        if (steps >= 32 && clusters <= 15) parts = 8;
+        return {parts > 1 ? kSplits : kAlone, true, parts};
+    }
+    return {rows > 128 ? kPairs : kAlone, false, 1};
+}
+
+template <int kForm, int kScales>
+mx_status launch_planned(const Plan &p, const Maps &maps, const MatArgs &a, cudaStream_t stream) {
+    if (p.work == kPairs) return launch_product<kForm, kScales, 256, kPairs>(maps, a, 1, stream);
+    if (p.work == kSplits) return launch_product<kForm, kScales, 128, kSplits>(maps, a, p.parts, stream);
+    return p.narrow ? launch_product<kForm, kScales, 128, kAlone>(maps, a, 1, stream)
+                    : launch_product<kForm, kScales, 256, kAlone>(maps, a, 1, stream);
 }
 
 bool operand_ok(const void *p, int64_t stride) { return aligned_to(p, 16) && stride % 16 == 0; }
@@ -716,11 +837,15 @@ mx_status mx_grouped_matmul_m(const void *a, mx_dtype a_dtype, int64_t a_stride,
     m.out_type = out_code(out_dtype);
     m.tma_out = aligned_to(out, 16) && (out_stride * os) % 16 == 0;
     m.idesc = block_scaled_idesc(a_dtype == MX_E5M2, b_dtype == MX_E5M2, false, !nk);
-    const bool pair = use_pair(div_up(rows, num_groups));
+    int sms = 0;
+    if (mx_status st = mx_device_sms(&sms); st != MX_OK) return st;
+    const int64_t each = div_up(rows, num_groups), even = div_up(each, 128) * num_groups;
+    const Plan plan = plan_of(even < rows ? even : rows, most_row_tiles(rows, num_groups, 128), n, each, m.k_tiles, sms);
+    const bool pair = plan.work == kPairs;
     Maps maps = {};
     if (mx_status st = operand_map(&maps.a, a, k, rows, a_stride, 0, 0, 128); st != MX_OK) return st;
     if (mx_status st = operand_map(&maps.b, b, nk ? k : n, nk ? n : k, b_stride, num_groups,
-                                   num_groups > 1 ? b_group_stride : b_stride, nk && !pair ? 256 : 128);
+                                   num_groups > 1 ? b_group_stride : b_stride, nk && !pair && !plan.narrow ? 256 : 128);
         st != MX_OK)
         return st;
     if (m.tma_out)
@@ -730,14 +855,10 @@ mx_status mx_grouped_matmul_m(const void *a, mx_dtype a_dtype, int64_t a_stride,
         if (a_tiles > INT_MAX || b_tiles > INT_MAX) return MX_ERR_UNSUPPORTED;
         if (mx_status st = tiles_map(&maps.sa, a_scales, a_tiles); st != MX_OK) return st;
         if (mx_status st = tiles_map(&maps.sb, b_scales, b_tiles); st != MX_OK) return st;
-        return pair ? launch_product<kFormNK, kScales32, 256, true>(maps, m, stream)
-                    : launch_product<kFormNK, kScales32, 256, false>(maps, m, stream);
+        return launch_planned<kFormNK, kScales32>(plan, maps, m, stream);
     }
-    if (nk)
-        return pair ? launch_product<kFormNK, kScales128, 256, true>(maps, m, stream)
-                    : launch_product<kFormNK, kScales128, 256, false>(maps, m, stream);
-    return pair ? launch_product<kFormKN, kScales128, 256, true>(maps, m, stream)
-                : launch_product<kFormKN, kScales128, 256, false>(maps, m, stream);
+    return nk ? launch_planned<kFormNK, kScales128>(plan, maps, m, stream)
+              : launch_planned<kFormKN, kScales128>(plan, maps, m, stream);
 }
 
 mx_status mx_grouped_matmul_k(const void *a, mx_dtype a_dtype, int64_t a_stride, const uint8_t *a_scales,
@@ -785,8 +906,11 @@ mx_status mx_grouped_matmul_k(const void *a, mx_dtype a_dtype, int64_t a_stride,
                                    (num_groups > 1 ? out_group_stride : out_stride) * os);
             st != MX_OK)
             return st;
-    return use_pair(m) ? launch_product<kFormOuter, kScales128, 256, true>(maps, g, stream)
-                       : launch_product<kFormOuter, kScales128, 256, false>(maps, g, stream);
+    int sms = 0;
+    if (mx_status st = mx_device_sms(&sms); st != MX_OK) return st;
+    const int64_t row_tiles = div_up(m, 128) * num_groups;
+    const Plan plan = plan_of(row_tiles, row_tiles, n, m, padded_rows / 128 / num_groups, sms);
+    return launch_planned<kFormOuter, kScales128>(plan, maps, g, stream);
 }
 
 }  // extern "C"

@@ -268,10 +268,8 @@ def test_offsets_past_32_bits(mxlib):
     b = operand(gen, (2, N, C), E4)
     sb = scales(gen, (2, ref.up(N, 128) // 128, ref.up(C, 128) // 128), E4)
     got = mxs.grouped_matmul(q, s, b, sb, order.group_ends)
-    one = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
     for r in sample.tolist():
         g = int(r >= T)
-        want = mxs.grouped_matmul(q[r:r + 1], s[r:r + 1], b[g:g + 1], sb[g:g + 1], one[1:])
-        # the same instructions in the same order, on tiles of either kernel
-        assert torch.equal(got[r:r + 1], want), r
+        x1, b1 = wide(q[r:r + 1], s[r:r + 1], 1, 128), wide(b[g], sb[g], 128, 128)
+        near(got[r:r + 1], x1 @ b1.t(), x1.abs() @ b1.t().abs(), C, torch.finfo(BF).eps)
     assert mxs.mx_device_flags() == 0
