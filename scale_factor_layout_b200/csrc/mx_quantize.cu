@@ -159,54 +159,67 @@ struct RowsArgs {
     bool e5m2;
 };
 
-// A CTA takes 256 columns of 8 to 32 rows, a warp 1 to 4 of them: 4 loads in
-// flight a lane, or fewer where there are too few rows to fill the SMs.  kOrder: row t is written to the rows row_of_slot[t, :], so a
-// token is read and rounded once however many experts it goes to.
-template <typename T, bool kWide, int kBlock, bool kOrder>
+// A CTA takes 32 * kPer columns of 8 to 32 rows, a warp 1 to 4 of them: that many
+// rows' loads are in flight a lane, fewer where there are too few rows to fill
+// the SMs.  A lane holds kPer consecutive elements: 16 where rows allow it (half
+// the shuffles, scales and stores of 8 for the same bytes), else 8.  kOrder: row
+// t is written to the rows row_of_slot[t, :], so a token is read and rounded once
+// however many experts it goes to.
+template <typename T, bool kWide, int kPer, int kBlock, bool kOrder>
 __global__ void __launch_bounds__(kQThreads)
 quantize_rows_kernel(const T *__restrict__ x, int64_t x_stride, RowsArgs a) {
+    constexpr int kEights = kPer / 8, kLanes = kBlock / kPer;   // lanes of a block
     grid_dependency_wait();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int64_t band = blockIdx.x / a.segments;
-    const int c = (int)(blockIdx.x - band * a.segments) * 256 + lane * 8;
+    const int c = (int)(blockIdx.x - band * a.segments) * (32 * kPer) + lane * kPer;
     const int64_t r0 = (band * 8 + w) * a.per_warp;
     const int fexp = a.e5m2 ? 15 : 8;
-    Eight<T> v[4];
+    Eight<T> v[4][kEights];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[i] = i < a.per_warp && r0 + i < a.in_rows ? load8<T, kWide>(x + (r0 + i) * x_stride, c, a.cols) : no_eight<T>();
-    }
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < kEights; ++h)
+            v[i][h] = i < a.per_warp && r0 + i < a.in_rows ? load8<T, kWide>(x + (r0 + i) * x_stride, c + 8 * h, a.cols) : no_eight<T>();
+    const bool scaler = lane % kLanes == 0;
+    const int64_t block_at = (int64_t)(c / kBlock) * a.scale_block;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if (i >= a.per_warp) break;
         Top<T> top;
-        raise(top, v[i]);
+#pragma unroll
+        for (int h = 0; h < kEights; ++h) raise(top, v[i][h]);
         uint32_t amax = top_of(top);
 #pragma unroll
-        for (int d = 1; d < kBlock / 8; d <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+        for (int d = 1; d < kLanes; d <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, d));
         const uint32_t byte = scale_byte(amax, fexp);
-        uint2 q = make_uint2(kNanBytes, kNanBytes);
-        if (byte != 255u) {
-            const float s = inverse_scale(byte);
-            float f[8];
-            floats_of(v[i], f);
+        uint2 q[kEights];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) f[u] *= s;
-            q = eight_bytes(f, a.e5m2);
+        for (int h = 0; h < kEights; ++h) {
+            q[h] = make_uint2(kNanBytes, kNanBytes);
+            if (byte != 255u) {
+                const float s = inverse_scale(byte);
+                float f[8];
+                floats_of(v[i][h], f);
+#pragma unroll
+                for (int u = 0; u < 8; ++u) f[u] *= s;
+                q[h] = eight_bytes(f, a.e5m2);
+            }
         }
+        auto store = [&](int64_t r) {
+            uint8_t *row = a.q + r * a.q_stride;
+            if constexpr (kPer == 16) *reinterpret_cast<uint4 *>(row + c) = make_uint4(q[0].x, q[0].y, q[kEights - 1].x, q[kEights - 1].y);
+            else store8<kWide>(row, c, a.cols, q[0]);
+            if (scaler) a.scales[r * a.scale_row + block_at] = (uint8_t)byte;
+        };
         const int64_t t = r0 + i;
         if (t < a.in_rows && c < a.cols) {
-            const bool scaler = lane % (kBlock / 8) == 0;
-            const int64_t block_at = (int64_t)(c / kBlock) * a.scale_block;
             if (!kOrder) {
-                store8<kWide>(a.q + t * a.q_stride, c, a.cols, q);
-                if (scaler) a.scales[t * a.scale_row + block_at] = (uint8_t)byte;
+                store(t);
             } else {
                 for (int j = 0; j < a.k; ++j) {
                     const int64_t r = a.row_of_slot[t * a.k + j];
-                    if (r < 0 || r >= a.out_rows) continue;
-                    store8<kWide>(a.q + r * a.q_stride, c, a.cols, q);
-                    if (scaler) a.scales[r * a.scale_row + block_at] = (uint8_t)byte;
+                    if (r >= 0 && r < a.out_rows) store(r);
                 }
             }
         }
@@ -214,12 +227,12 @@ quantize_rows_kernel(const T *__restrict__ x, int64_t x_stride, RowsArgs a) {
     if (kOrder) {   // rows behind the last group
         int64_t from = *a.last_end;
         if (from < 0) from = 0;
-        const int64_t units = (int64_t)a.segments * 32, n = (a.out_rows - from) * units;
+        const int64_t units = (a.cols + 7) / 8, n = (a.out_rows - from) * units;
         for (int64_t i = (int64_t)blockIdx.x * kQThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kQThreads) {
             const int64_t r = from + i / units;
             const int at = (int)(i % units) * 8;
             store8<kWide>(a.q + r * a.q_stride, at, a.cols, make_uint2(0u, 0u));
-            if (at < a.cols && at % kBlock == 0) a.scales[r * a.scale_row + (int64_t)(at / kBlock) * a.scale_block] = 0;
+            if (at % kBlock == 0) a.scales[r * a.scale_row + (int64_t)(at / kBlock) * a.scale_block] = 0;
         }
     }
 }
@@ -352,15 +365,15 @@ bool wide_ok(const void *x, int64_t x_stride, int64_t x_group, int es, const voi
            q_stride % 8 == 0 && q_group % 8 == 0;
 }
 
-template <typename T, bool kWide>
+template <typename T, bool kWide, int kPer>
 mx_status rows_typed(const void *x, int64_t x_stride, const RowsArgs &a, int block, int64_t grid, cudaStream_t stream) {
     const T *p = static_cast<const T *>(x);
     const bool order = a.row_of_slot != nullptr;
     if (block == 128)
-        return order ? launch(quantize_rows_kernel<T, kWide, 128, true>, grid, kQThreads, 0, stream, p, x_stride, a)
-                     : launch(quantize_rows_kernel<T, kWide, 128, false>, grid, kQThreads, 0, stream, p, x_stride, a);
-    return order ? launch(quantize_rows_kernel<T, kWide, 32, true>, grid, kQThreads, 0, stream, p, x_stride, a)
-                 : launch(quantize_rows_kernel<T, kWide, 32, false>, grid, kQThreads, 0, stream, p, x_stride, a);
+        return order ? launch(quantize_rows_kernel<T, kWide, kPer, 128, true>, grid, kQThreads, 0, stream, p, x_stride, a)
+                     : launch(quantize_rows_kernel<T, kWide, kPer, 128, false>, grid, kQThreads, 0, stream, p, x_stride, a);
+    return order ? launch(quantize_rows_kernel<T, kWide, kPer, 32, true>, grid, kQThreads, 0, stream, p, x_stride, a)
+                 : launch(quantize_rows_kernel<T, kWide, kPer, 32, false>, grid, kQThreads, 0, stream, p, x_stride, a);
 }
 
 template <typename T, bool kSquare>
@@ -415,7 +428,9 @@ mx_status mx_quantize_rows(const void *x, mx_dtype dtype, int64_t rows, int64_t 
     a.out_rows = order ? rows * choices : rows;
     a.cols = (int32_t)cols;
     a.k = choices;
-    a.segments = (int32_t)mx::div_up(cols, 256);
+    const bool wide = mx::wide_ok(x, x_stride, 0, es, q, q_stride, 0, cols);
+    const bool sixteen = wide && cols % 16 == 0 && mx::aligned_to(q, 16) && q_stride % 16 == 0;
+    a.segments = (int32_t)mx::div_up(cols, sixteen ? 512 : 256);
     a.e5m2 = out_dtype == MX_E5M2;
     int sms = 0;
     if (mx_status st = mx_device_sms(&sms); st != MX_OK) return st;
@@ -423,8 +438,10 @@ mx_status mx_quantize_rows(const void *x, mx_dtype dtype, int64_t rows, int64_t 
     while (a.per_warp > 1 && mx::div_up(rows, 8 * a.per_warp) * a.segments < 2 * sms) a.per_warp /= 2;
     const int64_t grid = mx::div_up(rows, 8 * a.per_warp) * a.segments;
     if (grid > INT_MAX) return MX_ERR_UNSUPPORTED;
-    const bool wide = mx::wide_ok(x, x_stride, 0, es, q, q_stride, 0, cols);
-#define MX_ROWS(T) (wide ? mx::rows_typed<T, true>(x, x_stride, a, block, grid, stream) : mx::rows_typed<T, false>(x, x_stride, a, block, grid, stream))
+#define MX_ROWS(T)                                                                      \
+    (sixteen ? mx::rows_typed<T, true, 16>(x, x_stride, a, block, grid, stream)         \
+     : wide  ? mx::rows_typed<T, true, 8>(x, x_stride, a, block, grid, stream)          \
+             : mx::rows_typed<T, false, 8>(x, x_stride, a, block, grid, stream))
     if (dtype == MX_F32) return MX_ROWS(float);
     if (dtype == MX_BF16) return MX_ROWS(__nv_bfloat16);
     return MX_ROWS(__half);
