@@ -747,6 +747,11 @@ mx_status out_map(CUtensorMap *map, const void *p, int64_t row_bytes, int64_t ro
     return mx_encode_map(map, p, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
+// A tile's contraction has to end well within the time limit of a wait, and a
+// row's bytes are an int in the stores.
+constexpr int64_t kMaxContraction = 1ll << 25;
+bool too_long(int64_t contraction, int64_t n, int out_bytes) { return contraction > kMaxContraction || n * out_bytes > INT_MAX; }
+
 int out_code(mx_dtype t) { return t == MX_F32 ? 0 : t == MX_BF16 ? 1 : t == MX_F16 ? 2 : -1; }
 bool eight(mx_dtype t) { return t == MX_E4M3 || t == MX_E5M2; }
 
@@ -817,6 +822,7 @@ mx_status mx_grouped_matmul_m(const void *a, mx_dtype a_dtype, int64_t a_stride,
     if (!operand_ok(a, a_stride) || !operand_ok(b, b_stride) || (num_groups > 1 && b_group_stride % 16 != 0) ||
         !aligned_to(out, os) || !aligned_to(group_ends, 4))
         return MX_ERR_MISALIGNED;
+    if (too_long(k, n, os)) return MX_ERR_UNSUPPORTED;
     if (block == 32 && (!aligned_to(a_scales, 16) || !aligned_to(b_scales, 16))) return MX_ERR_MISALIGNED;
 
     MatArgs m = {};
@@ -879,6 +885,8 @@ mx_status mx_grouped_matmul_k(const void *a, mx_dtype a_dtype, int64_t a_stride,
     const int os = out_dtype == MX_F32 ? 4 : 2;
     if (!operand_ok(a, a_stride) || !operand_ok(b, b_stride) || !aligned_to(out, os) || !aligned_to(group_ends, 4))
         return MX_ERR_MISALIGNED;
+
+    if (too_long(padded_rows, n, os)) return MX_ERR_UNSUPPORTED;
 
     MatArgs g = {};
     g.ends = group_ends;

@@ -1054,6 +1054,6 @@ mx_status mx_selftest_bounded_wait(int64_t limit_cycles, cudaStream_t stream) {
 
 int mx_last_cuda_error(void) { return (int)mx::t_last_error; }
 
-int mx_version(void) { return 100; }
+int mx_version(void) { return 200; }
 
 }  // extern "C"
