@@ -10,9 +10,12 @@
 // byte is e + 127, at least 0; a block that holds a NaN or an infinity gets
 // the byte 255 (NaN) and NaN elements.  A block of zeros gets the byte 0.
 //
-// Everything here is bound by memory.  A thread holds 8 consecutive elements
-// (one 16-byte load of 16-bit input, one 8-byte store), because a block of
-// 128 is then 16 neighbouring lanes and its maximum 4 shuffles.
+// Everything here is bound by memory.  A thread holds 8 or 16 consecutive
+// elements, because a block of 128 is then 16 or 8 neighbouring lanes and its
+// maximum 4 or 3 shuffles.  On a B200, 131072 x 7168 bf16: rows 411 us (6.85
+// TB/s; 8 elements a lane 522), columns of 8 groups 497 us (5.7 TB/s), 128 x 128
+// blocks 459 us (6.1 TB/s); 16384 tokens to 131072 rows in expert order 217 us
+// (5.4 TB/s), 23 of them for the scales, whose bytes go to scattered rows.
 
 #include <climits>
 
@@ -241,7 +244,9 @@ quantize_rows_kernel(const T *__restrict__ x, int64_t x_stride, RowsArgs a) {
 // 128 x 128 tiles, 256 threads: thread (ty, tx) holds rows ty + 16 i (i < 8) of
 // columns 8 tx .. 8 tx + 7, 8 loads in flight; a warp covers two rows of 128
 // columns.  Column blocks (one scale a column) and square blocks (one a tile)
-// differ in how far the maximum is reduced.
+// differ in how far the maximum is reduced.  Four CTAs an SM (16-bit input, 64
+// registers) overlap one tile's stores with another's loads: with two, columns
+// took 720 us where they take 497.
 struct TileArgs {
     int64_t x_stride, x_group;      // elements
     uint8_t *q;

@@ -207,7 +207,8 @@ def test_larger_products(mxlib, sizes, behind, N, K, ta, tb, out, form):
     assert got[begin:].eq(0).all() and mxs.mx_device_flags() == 0
 
 
-@pytest.mark.parametrize("sizes,M,N", [([1000, 0, 333, 5], 1000, 1300), ([700, 2000], 257, 288), ([3000], 1408, 520), ([60] * 64, 300, 272)])
+@pytest.mark.parametrize("sizes,M,N", [([1000, 0, 333, 5], 1000, 1300), ([700, 2000], 257, 288), ([3000], 1408, 520), ([60] * 64, 300, 272),
+                                       ([900, 0, 1300], 1400, 2560), ([2000, 500], 2560, 1400)])   # one of them is computed across
 @pytest.mark.parametrize("ta,tb,out", [(E5, E4, BF), (E4, E4, torch.float32)])
 def test_larger_weight_gradients(mxlib, sizes, M, N, ta, tb, out):
     gen = torch.Generator(device="cuda").manual_seed(M + N)
