@@ -179,8 +179,7 @@ __device__ __forceinline__ int warp_scan_sum(int v, int lane) {
 // two exclusive prefix sums give the padded starts and the work-item starts.
 //   M: padded size roundup(n, 128); items ceil(n / 128) * col_chunks.
 //   K: padded size roundup(w, 4);   items (chunks per row band) ceil(W / 128).
-// (kItemRows: rows of a work item where they are not those of a tile.)
-template <bool kDimM, int kItemRows = kTileRows>
+template <bool kDimM>
 __device__ __forceinline__ void build_group_table(const int32_t *__restrict__ ends, int G, int limit,
                                                   int col_chunks, GroupTable &t) {
     const int lane = threadIdx.x & 31;
@@ -204,8 +203,8 @@ __device__ __forceinline__ void build_group_table(const int32_t *__restrict__ en
     if (kDimM) {
         p0 = (n0 + 127) & ~127;
         p1 = (n1 + 127) & ~127;
-        i0 = (n0 + kItemRows - 1) / kItemRows * col_chunks;
-        i1 = (n1 + kItemRows - 1) / kItemRows * col_chunks;
+        i0 = (p0 >> 7) * col_chunks;
+        i1 = (p1 >> 7) * col_chunks;
     } else {
         p0 = (n0 + 3) & ~3;
         p1 = (n1 + 3) & ~3;

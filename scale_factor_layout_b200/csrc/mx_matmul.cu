@@ -124,10 +124,18 @@ struct Tile {
 // full one.
 struct Groups {
     int first0, first1;   // tiles of rows before the group
+    int tiles;            // of all groups
     int begin0, begin1, size0, size1, pstart0, pstart1;
-    __device__ __forceinline__ Groups(const GroupTable &t, int lane)
-        : first0(t.istart[lane]), first1(t.istart[lane + 32]), begin0(t.begin[lane]), begin1(t.begin[lane + 32]),
-          size0(t.size[lane]), size1(t.size[lane + 32]), pstart0(t.pstart[lane]), pstart1(t.pstart[lane + 32]) {}
+    __device__ __forceinline__ Groups(const GroupTable &t, int tile_rows, int lane)
+        : begin0(t.begin[lane]), begin1(t.begin[lane + 32]), size0(t.size[lane]), size1(t.size[lane + 32]),
+          pstart0(t.pstart[lane]), pstart1(t.pstart[lane + 32]) {
+        const int n0 = (size0 + tile_rows - 1) / tile_rows, n1 = (size1 + tile_rows - 1) / tile_rows;
+        const int s0 = warp_scan_sum(n0, lane);
+        const int s1 = warp_scan_sum(n1, lane) + __shfl_sync(0xffffffffu, s0, 31);
+        first0 = s0 - n0;
+        first1 = s1 - n1;
+        tiles = __shfl_sync(0xffffffffu, s1, 31);
+    }
     // the group of tile v of rows: the last one that starts at or before it
     __device__ __forceinline__ int find(int v) const {
         return __popc(__ballot_sync(0xffffffffu, first0 <= v)) + __popc(__ballot_sync(0xffffffffu, first1 <= v)) - 1;
@@ -441,14 +449,14 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
     __syncwarp();
     grid_dependency_wait();
     if (w == 3) tmem_alloc<kPair>(&sh.tmem, kTmemColumns);
-    if (w == 2) build_group_table<true, kTileRows>(a.ends, a.G, a.rows, 1, sh.table);
+    if (w == 2) build_group_table<true>(a.ends, a.G, a.rows, 1, sh.table);
     tc_fence_before();
     __syncthreads();
     if (kPair) cluster_sync();   // the barriers are there before the other CTA arrives on them
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    const Groups groups(sh.table, lane);
-    const int row_tiles = sh.table.istart[kMaxGroups];
+    const Groups groups(sh.table, kTileRows, lane);
+    const int row_tiles = groups.tiles;
     // tiles in all: the launch has an upper bound of blocks, the last of them without work
     const int total = kForm == kFormOuter ? a.G * a.m_tiles * a.n_tiles
                                           : (row_tiles + (a.rows - groups.last_end() + kTileRows - 1) / kTileRows) * a.n_tiles;
@@ -789,9 +797,12 @@ bool eight(mx_dtype t) { return t == MX_E4M3 || t == MX_E5M2; }
 // average; `steps`: of the contraction.
 struct Plan { Work work; bool narrow; int parts; };
 Plan plan_of(int64_t row_tiles, int64_t most, int64_t n, int64_t rows, int64_t steps, int sms) {
-    // 128 x 128 tiles where they fit the SMs at once, and of their contraction as
-    // many parts as clusters of that size run at once on a B200 (74 of 2 CTAs, 33
-    // of 4, 15 of 8: clusters do not cross the borders of its processor groups)
+    // 128 x 128 tiles where they fit the SMs at once (128 rows, 4 groups of 4096 x
+    // 4096, 128 of them: 18.6 us, 26.2 with tiles of 256 columns; 16 groups of 1408 x
+    // 1024, 176 of them: 12.0 and 9.7), and of their contraction as many parts as
+    // clusters of that size run at once on a B200 (74 of 2 CTAs, 33 of 4, 15 of 8:
+    // clusters do not cross the borders of its processor groups; one group of 1408 x
+    // 7168: 14.2 us in four parts, 23.6 whole)
     const int64_t tiles = row_tiles * div_up(n, 128);
     if (tiles <= sms) {
         const int64_t clusters = most * div_up(n, 128);
@@ -801,6 +812,9 @@ Plan plan_of(int64_t row_tiles, int64_t most, int64_t n, int64_t rows, int64_t s
         if (steps >= 32 && clusters <= 15) parts = 8;
         return {parts > 1 ? kSplits : kAlone, true, parts};
     }
+    // Pairs where groups have more than 128 rows on average: 32 groups of 2048 x 2048,
+    // with 64 rows each 31 us alone and 38 in pairs, 128: 33 and 40, 160: 44 and 44,
+    // 256: 50 and 44, 512: 75 and 75; 8192 rows of one 8192 x 8192: 420 and 385.
     return {rows > 128 ? kPairs : kAlone, false, 1};
 }
 
