@@ -178,6 +178,7 @@ def scales(gen, shape, dtype):
     ([1000, 0, 333], 700, 1000, 1300),     # 256-row tiles, a half-empty one, rows behind, narrow last columns
     ([129, 255, 256, 257, 511], 0, 288, 512), ([4000], 1, 2320, 144), ([5, 3000, 7, 1500], 0, 130, 2048),
     ([90] * 64, 33, 520, 400), ([300] * 64, 0, 96, 128),
+    ([20000, 5], 100, 1, 48), ([9000] * 3, 0, 40, 200),   # pairs on narrow tiles
     # many short tiles, ragged ends stored element by element, and a run of empty tiles at the end: a
     # warp still busy with its stores must not lose its next tile to the ones announced after it
     ([1187, 0, 1700, 1102, 742, 1326, 2740, 2043, 656, 426, 668, 1061, 208, 916, 453, 583], 490, 4080, 1408),

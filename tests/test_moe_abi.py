@@ -102,6 +102,7 @@ PRODUCT_K = dict(a=0x1000, a_dtype=B.MX_E4M3, a_stride=64, a_scales=0x2000, a_sc
     ("mx_grouped_matmul_m", PRODUCT, dict(block=32, b_layout=B.MX_B_KN, b_group_stride=4096), UNSUPPORTED),
     ("mx_grouped_matmul_m", PRODUCT, dict(k=2**25 + 16, a_stride=2**26, b_stride=2**26, b_group_stride=2**31), UNSUPPORTED),
     ("mx_grouped_matmul_m", PRODUCT, dict(n=2**30, out_stride=2**30, b_group_stride=2**36), UNSUPPORTED),
+    ("mx_grouped_matmul_m", PRODUCT, dict(b_stride=2**40, b_group_stride=2**62), UNSUPPORTED),
     ("mx_grouped_matmul_m", PRODUCT, dict(rows=0), OK),
     ("mx_grouped_matmul_k", PRODUCT_K, dict(padded_rows=200), INVALID),
     ("mx_grouped_matmul_k", PRODUCT_K, dict(padded_rows=0), INVALID),
