@@ -162,6 +162,35 @@ def test_threads_and_streams(mxlib):
     assert mxs.mx_device_flags() == 0
 
 
+def test_nothing_to_do(mxlib):
+    """No tokens, rows, columns or groups' rows: empty results, or zeros where a result has a size."""
+    dev = "cuda"
+    order = mxs.expert_sort(torch.zeros(0, 2, dtype=torch.int64, device=dev), 3)
+    assert order.group_ends.tolist() == [0, 0, 0] and order.row_of_slot.shape == (0, 2)
+    none = torch.empty(0, 40, device=dev, dtype=BF)
+    assert mxs.dispatch_rows(none, order).shape == (0, 40)
+    assert mxs.combine_rows(none, order).shape == (0, 40)
+    d_rows, d_w = mxs.combine_rows_backward(none, none, order, torch.empty(0, 2, device=dev))
+    assert d_rows.shape == (0, 40) and d_w.shape == (0, 2)
+    q, s = mxs.quantize_rows(none, order=order)
+    assert q.shape == (0, 40) and s.shape == (0, 1)
+    q, s = mxs.quantize_rows(torch.empty(5, 0, device=dev))
+    assert q.shape == (5, 0) and s.shape == (5, 0)
+    ends = torch.zeros(2, dtype=torch.int32, device=dev)
+    q, s = mxs.quantize_cols(none, ends)
+    assert q.shape == (256, 40) and q.float().eq(0).all() and s.eq(0).all()
+    got = mxs.grouped_matmul_k(q, s, q, s, ends)
+    assert got.shape == (2, 40, 40) and got.eq(0).all()
+    wq, ws = mxs.quantize_blocks(torch.randn(2, 24, 40, device=dev))
+    assert mxs.quantize_blocks(torch.empty(0, 24, 40, device=dev))[0].shape == (0, 24, 40)
+    assert mxs.grouped_matmul(*mxs.quantize_rows(none), wq, ws, ends).shape == (0, 24)
+    x = torch.randn(7, 40, device=dev, dtype=BF)
+    assert mxs.grouped_matmul(*mxs.quantize_rows(x), wq, ws, ends).eq(0).all()       # all rows behind the last group
+    empty = mxs.quantize_blocks(torch.empty(2, 0, 40, device=dev))
+    assert mxs.grouped_matmul(*mxs.quantize_rows(x), *empty, ends).shape == (7, 0)
+    assert mxs.mx_device_flags() == 0
+
+
 def operand(gen, shape, dtype):
     v = (torch.randn(shape, device="cuda", generator=gen) * (60 if dtype is E4 else 8000)).to(dtype)
     buf = torch.zeros((*shape[:-1], ref.up(shape[-1], 16)), dtype=torch.uint8, device="cuda").view(dtype)
