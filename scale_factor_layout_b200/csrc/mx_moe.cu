@@ -164,9 +164,11 @@ sort_place_kernel(const Id *__restrict__ ids, int64_t S, int64_t per_cta, int64_
 }
 
 // ------------------------------------------------------------------ rows
-// A CTA of 256 threads takes 256 / tpr tokens and one chunk of tpr packs of
-// their rows (tpr a power of two: the packs of a row, at most 256).  Chunks of
-// a token are neighbours in the grid, so their rows are touched together.
+// A CTA of 256 threads takes 256 / tpr tokens and one chunk of their rows: kPacks
+// packs a thread, tpr packs apart (tpr a power of two: the packs of a row, at
+// most 256).  Chunks of a token are neighbours in the grid, so their rows are
+// touched together.  A pack is 16 bytes, 4, or one element, whichever all rows
+// are aligned to.
 constexpr int kRowThreads = 256;
 
 struct RowShape {
@@ -176,6 +178,10 @@ struct RowShape {
     int32_t tpr_log2;
     int32_t chunks;
 };
+
+// Packs of a thread that are in flight for each row: enough small loads, and
+// enough of 16 bytes where a token has few rows.
+constexpr int packs_of(int bytes, int ahead) { return bytes == 16 ? 8 / ahead : ahead == 1 ? 4 : ahead == 2 ? 8 : 4; }
 
 template <typename P>
 __device__ __forceinline__ void zero_rows(P *__restrict__ out, int64_t stride, int64_t from, const RowShape &s) {
@@ -189,45 +195,61 @@ __device__ __forceinline__ void zero_rows(P *__restrict__ out, int64_t stride, i
     }
 }
 
+// This thread's token and first pack.
+template <int kPacks>
+__device__ __forceinline__ void place_of(const RowShape &s, int64_t &t, int &p) {
+    const int64_t slab = blockIdx.x / s.chunks;
+    const int chunk = (int)(blockIdx.x - slab * s.chunks);
+    t = (slab << (8 - s.tpr_log2)) + (threadIdx.x >> s.tpr_log2);
+    p = chunk * (kPacks << s.tpr_log2) + (threadIdx.x & ((1 << s.tpr_log2) - 1));
+}
+
 // out[row_of_slot[t, j]] = x[t]; rows from *last_end on = 0.  Strides in packs.
+constexpr int dispatch_packs(int bytes) { return bytes == 16 ? 1 : 4; }
 template <typename P>
 __global__ void __launch_bounds__(kRowThreads)
 dispatch_kernel(const P *__restrict__ x, int64_t x_stride, const int *__restrict__ row_of_slot,
                 const int *__restrict__ last_end, P *__restrict__ out, int64_t out_stride, RowShape s) {
+    constexpr int kPacks = dispatch_packs(sizeof(P));
     grid_dependency_wait();
-    const int64_t slab = blockIdx.x / s.chunks;
-    const int chunk = (int)(blockIdx.x - slab * s.chunks);
-    const int64_t t = (slab << (8 - s.tpr_log2)) + (threadIdx.x >> s.tpr_log2);
-    const int p = (chunk << s.tpr_log2) + (threadIdx.x & ((1 << s.tpr_log2) - 1));
-    if (t < s.tokens && p < s.packs) {
-        const P v = x[t * x_stride + p];
+    int64_t t;
+    int p;
+    place_of<kPacks>(s, t, p);
+    if (t < s.tokens) {
+        const int tpr = 1 << s.tpr_log2;
+        P v[kPacks];
+#pragma unroll
+        for (int i = 0; i < kPacks; ++i)
+            if (p + i * tpr < s.packs) v[i] = x[t * x_stride + p + i * tpr];
         const int *rows = row_of_slot + t * s.k;
         for (int j = 0; j < s.k; ++j) {
             const int64_t r = rows[j];
-            if (r >= 0 && r < s.rows) out[r * out_stride + p] = v;
+            if (r < 0 || r >= s.rows) continue;
+#pragma unroll
+            for (int i = 0; i < kPacks; ++i)
+                if (p + i * tpr < s.packs) out[r * out_stride + p + i * tpr] = v[i];
         }
     }
     zero_rows(out, out_stride, (int64_t)*last_end, s);
 }
 
-// y[t] = sum_j w[t, j] * rows[row_of_slot[t, j]] over the slots that have a row.
-template <typename T, int N>
+// y[t] = sum_j w[t, j] * rows[row_of_slot[t, j]] over the slots that have a row;
+// kAhead rows' loads are in flight together.  Strides in packs.
+template <typename T, int N, int kAhead>
 __global__ void __launch_bounds__(kRowThreads)
-combine_kernel(const T *__restrict__ rows, int64_t rows_stride, const int *__restrict__ row_of_slot,
-               const float *__restrict__ weights, T *__restrict__ y, int64_t y_stride, RowShape s) {
+combine_kernel(const Raw<T, N> *__restrict__ rows, int64_t rows_stride, const int *__restrict__ row_of_slot,
+               const float *__restrict__ weights, Raw<T, N> *__restrict__ y, int64_t y_stride, RowShape s) {
     using P = Raw<T, N>;
+    constexpr int kPacks = packs_of(sizeof(P), kAhead);
     grid_dependency_wait();
-    const int64_t slab = blockIdx.x / s.chunks;
-    const int chunk = (int)(blockIdx.x - slab * s.chunks);
-    const int64_t t = (slab << (8 - s.tpr_log2)) + (threadIdx.x >> s.tpr_log2);
-    const int p = (chunk << s.tpr_log2) + (threadIdx.x & ((1 << s.tpr_log2) - 1));
+    int64_t t;
+    int p;
+    place_of<kPacks>(s, t, p);
     if (t >= s.tokens || p >= s.packs) return;
-    float sum[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) sum[i] = 0.f;
-    constexpr int kAhead = 8;   // rows whose loads are in flight together
+    const int tpr = 1 << s.tpr_log2;
+    float sum[kPacks][N] = {};
     for (int j0 = 0; j0 < s.k; j0 += kAhead) {
-        P v[kAhead];
+        P v[kAhead][kPacks];
         float w[kAhead];
         bool live[kAhead];
 #pragma unroll
@@ -237,33 +259,40 @@ combine_kernel(const T *__restrict__ rows, int64_t rows_stride, const int *__res
             live[u] = r >= 0 && r < s.rows;
             w[u] = 1.f;
             if (live[u]) {
-                v[u] = *reinterpret_cast<const P *>(rows + r * rows_stride + (int64_t)p * N);
+#pragma unroll
+                for (int i = 0; i < kPacks; ++i)
+                    if (p + i * tpr < s.packs) v[u][i] = rows[r * rows_stride + p + i * tpr];
                 if (weights != nullptr) w[u] = weights[slot];
             }
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
             if (live[u]) {
-                float f[N];
-                unpack<T, N>(v[u], f);
 #pragma unroll
-                for (int i = 0; i < N; ++i) sum[i] = fmaf(w[u], f[i], sum[i]);
+                for (int i = 0; i < kPacks; ++i) {
+                    float f[N];
+                    unpack<T, N>(v[u][i], f);
+#pragma unroll
+                    for (int e = 0; e < N; ++e) sum[i][e] = fmaf(w[u], f[e], sum[i][e]);
+                }
             }
     }
-    *reinterpret_cast<P *>(y + t * y_stride + (int64_t)p * N) = pack<T, N>(sum);
+#pragma unroll
+    for (int i = 0; i < kPacks; ++i)
+        if (p + i * tpr < s.packs) y[t * y_stride + p + i * tpr] = pack<T, N>(sum[i]);
 }
 
 // d_rows[row_of_slot[t, j]] = w[t, j] * grad[t]; d_weights[t, j] = <grad[t], rows[...]>.
 // kTpt threads take one token and walk its whole row, because the inner
 // products run over it: a warp a token for short rows, a CTA for long ones.
-template <typename T, int N, int kTpt>
+template <typename T, int N, int kTpt, int kAhead>
 __global__ void __launch_bounds__(kRowThreads)
-combine_backward_kernel(const T *__restrict__ grad, int64_t grad_stride, const T *__restrict__ rows,
+combine_backward_kernel(const Raw<T, N> *__restrict__ grad, int64_t grad_stride, const Raw<T, N> *__restrict__ rows,
                         int64_t rows_stride, const int *__restrict__ row_of_slot, const int *__restrict__ last_end,
-                        const float *__restrict__ weights, T *__restrict__ d_rows, int64_t d_rows_stride,
+                        const float *__restrict__ weights, Raw<T, N> *__restrict__ d_rows, int64_t d_rows_stride,
                         float *__restrict__ d_weights, RowShape s) {
     using P = Raw<T, N>;
-    constexpr int kAhead = 8;
+    constexpr int kPacks = packs_of(sizeof(P), kAhead);
     __shared__ float part[kRowThreads / 32][kAhead];
     grid_dependency_wait();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -282,25 +311,36 @@ combine_backward_kernel(const T *__restrict__ grad, int64_t grad_stride, const T
                 wt[u] = live[u] ? weights[slot] : 0.f;
                 dot[u] = 0.f;
             }
-            for (int p = threadIdx.x % kTpt; p < s.packs; p += kTpt) {
-                float g[N];
-                unpack<T, N>(*reinterpret_cast<const P *>(grad + t * grad_stride + (int64_t)p * N), g);
-                P v[kAhead];
+            for (int p = threadIdx.x % kTpt; p < s.packs; p += kTpt * kPacks) {
+                P g[kPacks], v[kAhead][kPacks];
 #pragma unroll
-                for (int u = 0; u < kAhead; ++u)
-                    if (live[u]) v[u] = *reinterpret_cast<const P *>(rows + at[u] * rows_stride + (int64_t)p * N);
+                for (int i = 0; i < kPacks; ++i)
+                    if (p + i * kTpt < s.packs) g[i] = grad[t * grad_stride + p + i * kTpt];
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u)
                     if (live[u]) {
-                        float f[N], o[N];
-                        unpack<T, N>(v[u], f);
 #pragma unroll
-                        for (int i = 0; i < N; ++i) {
-                            dot[u] = fmaf(g[i], f[i], dot[u]);
-                            o[i] = wt[u] * g[i];
-                        }
-                        *reinterpret_cast<P *>(d_rows + at[u] * d_rows_stride + (int64_t)p * N) = pack<T, N>(o);
+                        for (int i = 0; i < kPacks; ++i)
+                            if (p + i * kTpt < s.packs) v[u][i] = rows[at[u] * rows_stride + p + i * kTpt];
                     }
+#pragma unroll
+                for (int i = 0; i < kPacks; ++i) {
+                    if (p + i * kTpt >= s.packs) break;
+                    float gf[N];
+                    unpack<T, N>(g[i], gf);
+#pragma unroll
+                    for (int u = 0; u < kAhead; ++u)
+                        if (live[u]) {
+                            float f[N], o[N];
+                            unpack<T, N>(v[u][i], f);
+#pragma unroll
+                            for (int e = 0; e < N; ++e) {
+                                dot[u] = fmaf(gf[e], f[e], dot[u]);
+                                o[e] = wt[u] * gf[e];
+                            }
+                            d_rows[at[u] * d_rows_stride + p + i * kTpt] = pack<T, N>(o);
+                        }
+                }
             }
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
@@ -325,8 +365,7 @@ combine_backward_kernel(const T *__restrict__ grad, int64_t grad_stride, const T
             }
         }
     }
-    RowShape z = s;
-    zero_rows(reinterpret_cast<P *>(d_rows), d_rows_stride / N, (int64_t)*last_end, z);
+    zero_rows(d_rows, d_rows_stride, (int64_t)*last_end, s);
 }
 
 // ------------------------------------------------------------------ host side
@@ -359,63 +398,67 @@ mx_status sort_typed(const void *ids, int64_t S, int32_t E, int32_t *group_ends,
                   static_cast<const int *>(ctas > 1 ? workspace : nullptr), group_ends, row_of_slot, slot_of_row);
 }
 
-// Elements of a pack: 16 bytes where every row of every matrix starts on a
-// 16-byte boundary and holds whole packs, one element otherwise.
+// Bytes of a pack: the most of 16 and 4 that every row of every matrix starts on
+// and is made of, else one element's.
 struct Mat { const void *p; int64_t stride; };
 template <int n>
-int pack_elements(int es, int64_t cols, const Mat (&m)[n]) {
-    const int N = 16 / es;
-    if (cols % N != 0) return 1;
-    for (const Mat &a : m)
-        if (!aligned_to(a.p, 16) || a.stride % N != 0) return 1;
-    return N;
+int pack_bytes(int es, int64_t cols, const Mat (&m)[n]) {
+    for (int bytes : {16, 4}) {
+        bool fits = cols * es % bytes == 0;
+        for (const Mat &a : m) fits = fits && aligned_to(a.p, bytes) && a.stride * es % bytes == 0;
+        if (fits) return bytes;
+    }
+    return es;
 }
 
-mx_status row_shape(int64_t tokens, int32_t choices, int64_t packs, RowShape *s, int64_t *grid) {
+mx_status row_shape(int64_t tokens, int32_t choices, int64_t packs, int per_thread, RowShape *s, int64_t *grid) {
     s->tokens = tokens;
     s->rows = tokens * choices;
     s->k = choices;
     s->packs = (int32_t)packs;
     s->tpr_log2 = 0;
-    while (s->tpr_log2 < 8 && (1 << s->tpr_log2) < packs) ++s->tpr_log2;
-    s->chunks = (int32_t)div_up(packs, 1ll << s->tpr_log2);
+    while (s->tpr_log2 < 8 && (per_thread << s->tpr_log2) < packs) ++s->tpr_log2;
+    s->chunks = (int32_t)div_up(packs, (int64_t)per_thread << s->tpr_log2);
     *grid = div_up(tokens, kRowThreads >> s->tpr_log2) * s->chunks;
     return *grid > INT_MAX ? MX_ERR_UNSUPPORTED : MX_OK;
 }
 
 template <typename P>
-mx_status dispatch_typed(const void *x, int64_t x_stride, const int32_t *row_of_slot, const int32_t *last_end, void *out,
-                         int64_t out_stride, int64_t tokens, int32_t choices, int64_t packs, cudaStream_t stream) {
+mx_status dispatch_typed(const void *x, int64_t x_bytes, const int32_t *row_of_slot, const int32_t *last_end, void *out,
+                         int64_t out_bytes, int64_t tokens, int32_t choices, int64_t row_bytes, cudaStream_t stream) {
+    constexpr int64_t n = sizeof(P);
     RowShape s;
     int64_t grid;
-    if (mx_status st = row_shape(tokens, choices, packs, &s, &grid); st != MX_OK) return st;
-    return launch(dispatch_kernel<P>, grid, kRowThreads, 0, stream, static_cast<const P *>(x), x_stride, row_of_slot,
-                  last_end, static_cast<P *>(out), out_stride, s);
+    if (mx_status st = row_shape(tokens, choices, row_bytes / n, dispatch_packs(n), &s, &grid); st != MX_OK) return st;
+    return launch(dispatch_kernel<P>, grid, kRowThreads, 0, stream, static_cast<const P *>(x), x_bytes / n, row_of_slot,
+                  last_end, static_cast<P *>(out), out_bytes / n, s);
 }
 
-template <typename T, int N>
+template <typename T, int N, int kAhead>
 mx_status combine_typed(const void *rows, int64_t rows_stride, const int32_t *row_of_slot, const float *weights, void *y,
                         int64_t y_stride, int64_t tokens, int32_t choices, int64_t cols, cudaStream_t stream) {
+    using P = Raw<T, N>;
     RowShape s;
     int64_t grid;
-    if (mx_status st = row_shape(tokens, choices, cols / N, &s, &grid); st != MX_OK) return st;
-    return launch(combine_kernel<T, N>, grid, kRowThreads, 0, stream, static_cast<const T *>(rows), rows_stride,
-                  row_of_slot, weights, static_cast<T *>(y), y_stride, s);
+    if (mx_status st = row_shape(tokens, choices, cols / N, packs_of(sizeof(P), kAhead), &s, &grid); st != MX_OK) return st;
+    return launch(combine_kernel<T, N, kAhead>, grid, kRowThreads, 0, stream, static_cast<const P *>(rows), rows_stride / N,
+                  row_of_slot, weights, static_cast<P *>(y), y_stride / N, s);
 }
 
-template <typename T, int N>
+template <typename T, int N, int kAhead>
 mx_status backward_typed(const void *grad, int64_t grad_stride, const void *rows, int64_t rows_stride,
                          const int32_t *row_of_slot, const int32_t *last_end, const float *weights, void *d_rows,
                          int64_t d_rows_stride, float *d_weights, int64_t tokens, int32_t choices, int64_t cols,
                          cudaStream_t stream) {
+    using P = Raw<T, N>;
     RowShape s;
     int64_t grid;
-    if (mx_status st = row_shape(tokens, choices, cols / N, &s, &grid); st != MX_OK) return st;
-    const bool warp = s.packs <= 128;
+    if (mx_status st = row_shape(tokens, choices, cols / N, 1, &s, &grid); st != MX_OK) return st;
+    const bool warp = s.packs <= 128 * packs_of(sizeof(P), kAhead);
     const int64_t ctas = warp ? div_up(tokens, kRowThreads / 32) : tokens;
-    return launch(warp ? combine_backward_kernel<T, N, 32> : combine_backward_kernel<T, N, kRowThreads>, ctas,
-                  kRowThreads, 0, stream, static_cast<const T *>(grad), grad_stride, static_cast<const T *>(rows),
-                  rows_stride, row_of_slot, last_end, weights, static_cast<T *>(d_rows), d_rows_stride, d_weights, s);
+    return launch(warp ? combine_backward_kernel<T, N, 32, kAhead> : combine_backward_kernel<T, N, kRowThreads, kAhead>, ctas,
+                  kRowThreads, 0, stream, static_cast<const P *>(grad), grad_stride / N, static_cast<const P *>(rows),
+                  rows_stride / N, row_of_slot, last_end, weights, static_cast<P *>(d_rows), d_rows_stride / N, d_weights, s);
 }
 
 }  // namespace
@@ -462,11 +505,10 @@ mx_status mx_dispatch_rows(const void *x, mx_dtype dtype, int64_t tokens, int64_
     if (mx_status st = mx_device_sms(&sms); st != MX_OK) return st;
     const int32_t *last = group_ends + num_experts - 1;
     const mx::Mat mats[] = {{x, x_stride}, {out, out_stride}};
-    const int N = mx::pack_elements(es, cols, mats);
-    if (N > 1)
-        return mx::dispatch_typed<uint4>(x, x_stride / N, row_of_slot, last, out, out_stride / N, tokens, choices, cols / N, stream);
-    return es == 4 ? mx::dispatch_typed<uint32_t>(x, x_stride, row_of_slot, last, out, out_stride, tokens, choices, cols, stream)
-                   : mx::dispatch_typed<uint16_t>(x, x_stride, row_of_slot, last, out, out_stride, tokens, choices, cols, stream);
+#define MX_DISPATCH(P) mx::dispatch_typed<P>(x, x_stride * es, row_of_slot, last, out, out_stride * es, tokens, choices, cols * es, stream)
+    const int bytes = mx::pack_bytes(es, cols, mats);
+    return bytes == 16 ? MX_DISPATCH(uint4) : bytes == 4 ? MX_DISPATCH(uint32_t) : MX_DISPATCH(uint16_t);
+#undef MX_DISPATCH
 }
 
 mx_status mx_combine_rows(const void *rows, mx_dtype dtype, int64_t tokens, int64_t cols, int64_t rows_stride,
@@ -482,12 +524,15 @@ mx_status mx_combine_rows(const void *rows, mx_dtype dtype, int64_t tokens, int6
     int sms = 0;
     if (mx_status st = mx_device_sms(&sms); st != MX_OK) return st;
     const mx::Mat mats[] = {{rows, rows_stride}, {y, y_stride}};
-    const bool wide = mx::pack_elements(es, cols, mats) > 1;
-#define MX_COMBINE(T, N) mx::combine_typed<T, N>(rows, rows_stride, row_of_slot, weights, y, y_stride, tokens, choices, cols, stream)
-    if (dtype == MX_F32) return wide ? MX_COMBINE(float, 4) : MX_COMBINE(float, 1);
-    if (dtype == MX_BF16) return wide ? MX_COMBINE(__nv_bfloat16, 8) : MX_COMBINE(__nv_bfloat16, 1);
-    return wide ? MX_COMBINE(__half, 8) : MX_COMBINE(__half, 1);
+    const int bytes = mx::pack_bytes(es, cols, mats);
+#define MX_COMBINE_K(T, N, K) mx::combine_typed<T, N, K>(rows, rows_stride, row_of_slot, weights, y, y_stride, tokens, choices, cols, stream)
+#define MX_COMBINE(T, N) (choices <= 2 ? MX_COMBINE_K(T, N, 2) : MX_COMBINE_K(T, N, 8))
+    if (dtype == MX_F32) return bytes == 16 ? MX_COMBINE(float, 4) : MX_COMBINE(float, 1);
+    if (dtype == MX_BF16)
+        return bytes == 16 ? MX_COMBINE(__nv_bfloat16, 8) : bytes == 4 ? MX_COMBINE(__nv_bfloat16, 2) : MX_COMBINE(__nv_bfloat16, 1);
+    return bytes == 16 ? MX_COMBINE(__half, 8) : bytes == 4 ? MX_COMBINE(__half, 2) : MX_COMBINE(__half, 1);
 #undef MX_COMBINE
+#undef MX_COMBINE_K
 }
 
 mx_status mx_combine_rows_backward(const void *grad, mx_dtype dtype, int64_t tokens, int64_t cols, int64_t grad_stride,
@@ -510,14 +555,17 @@ mx_status mx_combine_rows_backward(const void *grad, mx_dtype dtype, int64_t tok
     if (mx_status st = mx_device_sms(&sms); st != MX_OK) return st;
     const int32_t *last = group_ends + num_experts - 1;
     const mx::Mat mats[] = {{grad, grad_stride}, {rows, rows_stride}, {d_rows, d_rows_stride}};
-    const bool wide = mx::pack_elements(es, cols, mats) > 1;
-#define MX_BACKWARD(T, N)                                                                                              \
-    mx::backward_typed<T, N>(grad, grad_stride, rows, rows_stride, row_of_slot, last, weights, d_rows, d_rows_stride, \
-                             d_weights, tokens, choices, cols, stream)
-    if (dtype == MX_F32) return wide ? MX_BACKWARD(float, 4) : MX_BACKWARD(float, 1);
-    if (dtype == MX_BF16) return wide ? MX_BACKWARD(__nv_bfloat16, 8) : MX_BACKWARD(__nv_bfloat16, 1);
-    return wide ? MX_BACKWARD(__half, 8) : MX_BACKWARD(__half, 1);
+    const int bytes = mx::pack_bytes(es, cols, mats);
+#define MX_BACKWARD_K(T, N, K)                                                                                            \
+    mx::backward_typed<T, N, K>(grad, grad_stride, rows, rows_stride, row_of_slot, last, weights, d_rows, d_rows_stride, \
+                                d_weights, tokens, choices, cols, stream)
+#define MX_BACKWARD(T, N) (choices <= 2 ? MX_BACKWARD_K(T, N, 2) : MX_BACKWARD_K(T, N, 8))
+    if (dtype == MX_F32) return bytes == 16 ? MX_BACKWARD(float, 4) : MX_BACKWARD(float, 1);
+    if (dtype == MX_BF16)
+        return bytes == 16 ? MX_BACKWARD(__nv_bfloat16, 8) : bytes == 4 ? MX_BACKWARD(__nv_bfloat16, 2) : MX_BACKWARD(__nv_bfloat16, 1);
+    return bytes == 16 ? MX_BACKWARD(__half, 8) : bytes == 4 ? MX_BACKWARD(__half, 2) : MX_BACKWARD(__half, 1);
 #undef MX_BACKWARD
+#undef MX_BACKWARD_K
 }
 
 }  // extern "C"

@@ -42,14 +42,14 @@ template <> __device__ __forceinline__ float from_f32<float>(float v) { return v
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
-// N consecutive elements as one load or store moves them: 16 bytes, or one
-// element where rows do not start on 16-byte boundaries.  They stay words until
-// they are unpacked: arrays of 16-bit types are not always moved as a whole.
-template <typename T, int N> struct RawOf { using Type = uint4; };
-template <> struct RawOf<float, 1> { using Type = uint32_t; };
-template <> struct RawOf<__nv_bfloat16, 1> { using Type = uint16_t; };
-template <> struct RawOf<__half, 1> { using Type = uint16_t; };
-template <typename T, int N> using Raw = typename RawOf<T, N>::Type;
+// N consecutive elements as one load or store moves them: 16 bytes, 4, or one
+// element, as rows are aligned.  They stay words until they are unpacked: arrays
+// of 16-bit types are not always moved as a whole.
+template <int bytes> struct RawOf;
+template <> struct RawOf<16> { using Type = uint4; };
+template <> struct RawOf<4> { using Type = uint32_t; };
+template <> struct RawOf<2> { using Type = uint16_t; };
+template <typename T, int N> using Raw = typename RawOf<sizeof(T) * N>::Type;
 
 template <typename T> __device__ __forceinline__ float2 two_floats(uint32_t w);
 template <> __device__ __forceinline__ float2 two_floats<__nv_bfloat16>(uint32_t w) {
@@ -74,6 +74,9 @@ __device__ __forceinline__ void unpack(const Raw<T, N> &r, float (&f)[N]) {
         f[0] = __uint_as_float(r);
     } else if constexpr (N == 1) {
         f[0] = two_floats<T>(r).x;
+    } else if constexpr (N == 2) {
+        const float2 a = two_floats<T>(r);
+        f[0] = a.x, f[1] = a.y;
     } else if constexpr (sizeof(T) == 4) {
         f[0] = __uint_as_float(r.x), f[1] = __uint_as_float(r.y), f[2] = __uint_as_float(r.z), f[3] = __uint_as_float(r.w);
     } else {
@@ -87,6 +90,8 @@ __device__ __forceinline__ Raw<T, N> pack(const float (&f)[N]) {
         return __float_as_uint(f[0]);
     } else if constexpr (N == 1) {
         return (uint16_t)two_packed<T>(f[0], 0.f);
+    } else if constexpr (N == 2) {
+        return two_packed<T>(f[0], f[1]);
     } else if constexpr (sizeof(T) == 4) {
         return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
     } else {
