@@ -250,10 +250,10 @@ __device__ __forceinline__ uint4 tile_line(const uint32_t (&b)[16]) {
 }
 
 template <typename T>
-__device__ __forceinline__ void store_row(void *out, int64_t at, const uint32_t *v, int valid, bool wide) {
+__device__ __forceinline__ void store_row(void *out, int64_t at, const uint32_t *v, int valid) {
     T *dst = static_cast<T *>(out) + at;
     constexpr int N = 16 / sizeof(T);
-    if (wide && valid >= 32) {
+    if (valid >= 32) {
 #pragma unroll
         for (int i = 0; i < 32; i += N) {
             float f[N];
@@ -289,6 +289,18 @@ __device__ __forceinline__ void stage_row(uint8_t *box, const uint32_t *v, int l
         for (int u = 0; u < N; ++u) f[u] = __uint_as_float(v[c * N + u]);
         *reinterpret_cast<uint4 *>(box + lane * kOutRow + ((c ^ (lane >> 1 & 3)) << 4)) = pack<T, N>(f);
     }
+}
+
+// The box's rows into rows of `out` that start anywhere: a half or whole warp
+// writes the 64 bytes of a row, so that a store touches two lines at most and not
+// 32.
+template <typename W>
+__device__ __forceinline__ void store_box(const uint8_t *box, W *out, int64_t at, int64_t stride, int rows, int cols, int lane) {
+    constexpr int kLine = kOutRow / sizeof(W), kAtOnce = 32 / kLine;   // elements of a row; rows of a store
+    const int e = lane % kLine, piece = e * sizeof(W) / 16, byte = e * sizeof(W) % 16;
+#pragma unroll 8
+    for (int r = lane / kLine; r < rows; r += kAtOnce)
+        if (e < cols) out[at + r * stride + e] = *reinterpret_cast<const W *>(box + r * kOutRow + ((piece ^ (r >> 1 & 3)) << 4) + byte);
 }
 
 // The tiles of a CTA (of a pair).  The first is its own block's; for each that it
@@ -648,13 +660,14 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
                 continue;
             }
             const int r0 = quarter * 32, n0 = o.n0 + part_of_columns * kCols, es = a.out_type == 0 ? 4 : 2;
+            const int wanted = a.N - n0;   // columns from n0 on that exist
             if (kForm == kFormOuter && kPair && a.swapped) {
                 // a lane's row is a column of out: 32 lanes write 32 neighbours of each of their columns
                 const int64_t at = o.g * a.out_group + (int64_t)n0 * a.out_stride + o.row0 + r0 + lane;
                 if (r0 + lane < o.rows) {
-                    if (a.out_type == 0) store_across<float, kCols>(a.out, at, a.out_stride, v, a.N - n0);
-                    else if (a.out_type == 1) store_across<__nv_bfloat16, kCols>(a.out, at, a.out_stride, v, a.N - n0);
-                    else store_across<__half, kCols>(a.out, at, a.out_stride, v, a.N - n0);
+                    if (a.out_type == 0) store_across<float, kCols>(a.out, at, a.out_stride, v, wanted);
+                    else if (a.out_type == 1) store_across<__nv_bfloat16, kCols>(a.out, at, a.out_stride, v, wanted);
+                    else store_across<__half, kCols>(a.out, at, a.out_stride, v, wanted);
                 }
             } else if (a.tma_out && r0 + 32 <= o.rows) {
                 // whole rows of the warp: through shared memory, since a lane holds a row and
@@ -663,7 +676,7 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
 #pragma unroll
                 for (int c = 0; c < kCols; c += 16) {
                     if (es == 2 && c % 32 != 0) continue;
-                    if (n0 + c >= a.N) break;
+                    if (c >= wanted) break;
                     if (lane == 0) bulk_wait_read<0>();   // the box is free
                     __syncwarp();
                     if (a.out_type == 0) stage_row<float>(box, v + c, lane);
@@ -676,14 +689,32 @@ grouped_product(const __grid_constant__ Maps maps, const MatArgs a) {
                         bulk_commit();
                     }
                 }
-            } else if (r0 + lane < o.rows) {
-                const int64_t at = (kForm == kFormOuter ? o.g * a.out_group : 0) + (int64_t)(o.row0 + r0 + lane) * a.out_stride + n0;
+            } else if (a.tma_out) {   // some rows of the warp
+                if (r0 + lane < o.rows) {
+                    const int64_t at = (kForm == kFormOuter ? o.g * a.out_group : 0) + (int64_t)(o.row0 + r0 + lane) * a.out_stride + n0;
 #pragma unroll
-                for (int c = 0; c < kCols; c += 32) {
-                    const int valid = a.N - n0 - c;
-                    if (a.out_type == 0) store_row<float>(a.out, at + c, v + c, valid, a.tma_out);
-                    else if (a.out_type == 1) store_row<__nv_bfloat16>(a.out, at + c, v + c, valid, a.tma_out);
-                    else store_row<__half>(a.out, at + c, v + c, valid, a.tma_out);
+                    for (int c = 0; c < kCols; c += 32) {
+                        const int valid = wanted - c;
+                        if (a.out_type == 0) store_row<float>(a.out, at + c, v + c, valid);
+                        else if (a.out_type == 1) store_row<__nv_bfloat16>(a.out, at + c, v + c, valid);
+                        else store_row<__half>(a.out, at + c, v + c, valid);
+                    }
+                }
+            } else if (r0 < o.rows) {
+                uint8_t *box = sh.out[w - 4];
+                const int rows = min(32, o.rows - r0);
+                const int64_t at = (kForm == kFormOuter ? o.g * a.out_group : 0) + (int64_t)(o.row0 + r0) * a.out_stride + n0;
+#pragma unroll
+                for (int c = 0; c < kCols; c += 16) {
+                    if (es == 2 && c % 32 != 0) continue;
+                    if (c >= wanted) break;
+                    if (a.out_type == 0) stage_row<float>(box, v + c, lane);
+                    else if (a.out_type == 1) stage_row<__nv_bfloat16>(box, v + c, lane);
+                    else stage_row<__half>(box, v + c, lane);
+                    __syncwarp();
+                    if (es == 4) store_box(box, static_cast<uint32_t *>(a.out), at + c, a.out_stride, rows, wanted - c, lane);
+                    else store_box(box, static_cast<uint16_t *>(a.out), at + c, a.out_stride, rows, wanted - c, lane);
+                    __syncwarp();
                 }
             }
         } while (!kSplit && ok && tiles.next(lane));
