@@ -53,16 +53,19 @@ __device__ __forceinline__ uint2 eight_bytes(const float (&v)[8], bool e5m2) {
 constexpr uint32_t kNanBytes = 0x7f7f7f7fu;   // four NaNs in both types
 
 // Eight consecutive elements of a row from column c on, zeros past `cols`, as
-// the words that hold them.  kWide: rows start on 16-byte boundaries and cols is
-// a multiple of 8.
+// the words that hold them.  kIn: rows start on 16-byte boundaries (2), on 4-byte
+// ones (1), or anywhere (0); kWide, of the 8-bit rows, on 8-byte ones.
+enum In { kAnywhere = 0, kWords = 1, kVectors = 2 };
 template <typename T> struct Eight { uint4 q[sizeof(T) / 2]; };
-template <typename T, bool kWide>
+template <typename T, int kIn>
 __device__ __forceinline__ Eight<T> load8(const T *row, int c, int cols) {
     Eight<T> v;
-    if (kWide) {
+    if (kIn == kVectors && c + 8 <= cols) {
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-            v.q[i] = c < cols ? __ldg(reinterpret_cast<const uint4 *>(row + c) + i) : make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) v.q[i] = __ldg(reinterpret_cast<const uint4 *>(row + c) + i);
+    } else if (kIn == kWords && sizeof(T) == 2 && c + 8 <= cols) {
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(row + c);
+        v.q[0] = make_uint4(__ldg(src), __ldg(src + 1), __ldg(src + 2), __ldg(src + 3));
     } else {
         using W = Raw<T, 1>;
         const W *src = reinterpret_cast<const W *>(row);
@@ -139,8 +142,8 @@ template <typename T> __device__ __forceinline__ uint32_t top_of(const Top<T> &t
 
 template <bool kWide>
 __device__ __forceinline__ void store8(uint8_t *row, int c, int cols, uint2 q) {
-    if (kWide) {
-        if (c < cols) *reinterpret_cast<uint2 *>(row + c) = q;
+    if (kWide && c + 8 <= cols) {
+        *reinterpret_cast<uint2 *>(row + c) = q;
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -168,7 +171,7 @@ struct RowsArgs {
 // the shuffles, scales and stores of 8 for the same bytes), else 8.  kOrder: row
 // t is written to the rows row_of_slot[t, :], so a token is read and rounded once
 // however many experts it goes to.
-template <typename T, bool kWide, int kPer, int kBlock, bool kOrder>
+template <typename T, int kIn, bool kWide, int kPer, int kBlock, bool kOrder>
 __global__ void __launch_bounds__(kQThreads)
 quantize_rows_kernel(const T *__restrict__ x, int64_t x_stride, RowsArgs a) {
     constexpr int kEights = kPer / 8, kLanes = kBlock / kPer;   // lanes of a block
@@ -183,7 +186,7 @@ quantize_rows_kernel(const T *__restrict__ x, int64_t x_stride, RowsArgs a) {
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int h = 0; h < kEights; ++h)
-            v[i][h] = i < a.per_warp && r0 + i < a.in_rows ? load8<T, kWide>(x + (r0 + i) * x_stride, c + 8 * h, a.cols) : no_eight<T>();
+            v[i][h] = i < a.per_warp && r0 + i < a.in_rows ? load8<T, kIn>(x + (r0 + i) * x_stride, c + 8 * h, a.cols) : no_eight<T>();
     const bool scaler = lane % kLanes == 0;
     const int64_t block_at = (int64_t)(c / kBlock) * a.scale_block;
 #pragma unroll
@@ -259,7 +262,7 @@ struct TileArgs {
     bool e5m2;
 };
 
-template <typename T, bool kWide, bool kSquare>
+template <typename T, int kIn, bool kWide, bool kSquare>
 __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 4 : 2)
 quantize_tiles_kernel(const T *__restrict__ x, TileArgs a) {
     __shared__ alignas(16) uint32_t top[16][128];
@@ -301,7 +304,7 @@ quantize_tiles_kernel(const T *__restrict__ x, TileArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int r = ty + 16 * i;
-            v[i] = r < valid ? load8<T, kWide>(src + r * a.x_stride, c, a.cols) : no_eight<T>();
+            v[i] = r < valid ? load8<T, kIn>(src + r * a.x_stride, c, a.cols) : no_eight<T>();
         }
         Top<T> mine;
 #pragma unroll
@@ -364,39 +367,57 @@ quantize_tiles_kernel(const T *__restrict__ x, TileArgs a) {
 // ------------------------------------------------------------------ host side
 int in_bytes(mx_dtype t) { return t == MX_F32 ? 4 : t == MX_BF16 || t == MX_F16 ? 2 : 0; }
 
-bool wide_ok(const void *x, int64_t x_stride, int64_t x_group, int es, const void *q, int64_t q_stride, int64_t q_group,
-             int64_t cols) {
-    return cols % 8 == 0 && aligned_to(x, 16) && (x_stride * es) % 16 == 0 && (x_group * es) % 16 == 0 && aligned_to(q, 8) &&
-           q_stride % 8 == 0 && q_group % 8 == 0;
+// How rows of the input are aligned, and whether those of the output are.
+int in_of(const void *x, int64_t x_stride, int64_t x_group, int es) {
+    const auto on = [&](int64_t n) { return aligned_to(x, n) && x_stride * es % n == 0 && x_group * es % n == 0; };
+    return on(16) ? kVectors : es == 2 && on(4) ? kWords : kAnywhere;
+}
+bool wide_of(const void *q, int64_t q_stride, int64_t q_group, int64_t n) {
+    return aligned_to(q, n) && q_stride % n == 0 && q_group % n == 0;
 }
 
-template <typename T, bool kWide, int kPer>
+template <typename T, int kIn, bool kWide, int kPer>
 mx_status rows_typed(const void *x, int64_t x_stride, const RowsArgs &a, int block, int64_t grid, cudaStream_t stream) {
     const T *p = static_cast<const T *>(x);
     const bool order = a.row_of_slot != nullptr;
     if (block == 128)
-        return order ? launch(quantize_rows_kernel<T, kWide, kPer, 128, true>, grid, kQThreads, 0, stream, p, x_stride, a)
-                     : launch(quantize_rows_kernel<T, kWide, kPer, 128, false>, grid, kQThreads, 0, stream, p, x_stride, a);
-    return order ? launch(quantize_rows_kernel<T, kWide, kPer, 32, true>, grid, kQThreads, 0, stream, p, x_stride, a)
-                 : launch(quantize_rows_kernel<T, kWide, kPer, 32, false>, grid, kQThreads, 0, stream, p, x_stride, a);
+        return order ? launch(quantize_rows_kernel<T, kIn, kWide, kPer, 128, true>, grid, kQThreads, 0, stream, p, x_stride, a)
+                     : launch(quantize_rows_kernel<T, kIn, kWide, kPer, 128, false>, grid, kQThreads, 0, stream, p, x_stride, a);
+    return order ? launch(quantize_rows_kernel<T, kIn, kWide, kPer, 32, true>, grid, kQThreads, 0, stream, p, x_stride, a)
+                 : launch(quantize_rows_kernel<T, kIn, kWide, kPer, 32, false>, grid, kQThreads, 0, stream, p, x_stride, a);
+}
+
+// Rows of the output that are not aligned are rare (the torch calls align theirs): they share one kernel.
+template <typename T>
+mx_status rows_any(const void *x, int64_t x_stride, const RowsArgs &a, int block, int64_t grid, int in, bool wide, bool sixteen,
+                   cudaStream_t stream) {
+    if (sixteen) return rows_typed<T, kVectors, true, 16>(x, x_stride, a, block, grid, stream);
+    if (!wide) return rows_typed<T, kAnywhere, false, 8>(x, x_stride, a, block, grid, stream);
+    if (in == kVectors) return rows_typed<T, kVectors, true, 8>(x, x_stride, a, block, grid, stream);
+    if constexpr (sizeof(T) == 2)
+        if (in == kWords) return rows_typed<T, kWords, true, 8>(x, x_stride, a, block, grid, stream);
+    return rows_typed<T, kAnywhere, true, 8>(x, x_stride, a, block, grid, stream);
 }
 
 template <typename T, bool kSquare>
-mx_status tiles_typed(const void *x, const TileArgs &a, bool wide, cudaStream_t stream) {
+mx_status tiles_typed(const void *x, const TileArgs &a, int in, bool wide, cudaStream_t stream) {
     int sms = 0;
     if (mx_status st = mx_device_sms(&sms); st != MX_OK) return st;
     const int64_t cap = (int64_t)sms * 4;
     const int64_t grid = a.tiles < cap ? a.tiles : cap;
     const T *p = static_cast<const T *>(x);
-    return wide ? launch(quantize_tiles_kernel<T, true, kSquare>, grid, kQThreads, 0, stream, p, a)
-                : launch(quantize_tiles_kernel<T, false, kSquare>, grid, kQThreads, 0, stream, p, a);
+    if (!wide) return launch(quantize_tiles_kernel<T, kAnywhere, false, kSquare>, grid, kQThreads, 0, stream, p, a);
+    if (in == kVectors) return launch(quantize_tiles_kernel<T, kVectors, true, kSquare>, grid, kQThreads, 0, stream, p, a);
+    if constexpr (sizeof(T) == 2)
+        if (in == kWords) return launch(quantize_tiles_kernel<T, kWords, true, kSquare>, grid, kQThreads, 0, stream, p, a);
+    return launch(quantize_tiles_kernel<T, kAnywhere, true, kSquare>, grid, kQThreads, 0, stream, p, a);
 }
 
 template <bool kSquare>
-mx_status tiles_any(const void *x, mx_dtype dtype, const TileArgs &a, bool wide, cudaStream_t stream) {
-    if (dtype == MX_F32) return tiles_typed<float, kSquare>(x, a, wide, stream);
-    if (dtype == MX_BF16) return tiles_typed<__nv_bfloat16, kSquare>(x, a, wide, stream);
-    return tiles_typed<__half, kSquare>(x, a, wide, stream);
+mx_status tiles_any(const void *x, mx_dtype dtype, const TileArgs &a, int in, bool wide, cudaStream_t stream) {
+    if (dtype == MX_F32) return tiles_typed<float, kSquare>(x, a, in, wide, stream);
+    if (dtype == MX_BF16) return tiles_typed<__nv_bfloat16, kSquare>(x, a, in, wide, stream);
+    return tiles_typed<__half, kSquare>(x, a, in, wide, stream);
 }
 
 bool eight_bit_type(mx_dtype t) { return t == MX_E4M3 || t == MX_E5M2; }
@@ -433,8 +454,9 @@ mx_status mx_quantize_rows(const void *x, mx_dtype dtype, int64_t rows, int64_t 
     a.out_rows = order ? rows * choices : rows;
     a.cols = (int32_t)cols;
     a.k = choices;
-    const bool wide = mx::wide_ok(x, x_stride, 0, es, q, q_stride, 0, cols);
-    const bool sixteen = wide && cols % 16 == 0 && mx::aligned_to(q, 16) && q_stride % 16 == 0;
+    const int in = mx::in_of(x, x_stride, 0, es);
+    const bool wide = mx::wide_of(q, q_stride, 0, 8);
+    const bool sixteen = in == mx::kVectors && mx::wide_of(q, q_stride, 0, 16) && cols % 16 == 0;
     a.segments = (int32_t)mx::div_up(cols, sixteen ? 512 : 256);
     a.e5m2 = out_dtype == MX_E5M2;
     int sms = 0;
@@ -443,10 +465,7 @@ mx_status mx_quantize_rows(const void *x, mx_dtype dtype, int64_t rows, int64_t 
     while (a.per_warp > 1 && mx::div_up(rows, 8 * a.per_warp) * a.segments < 2 * sms) a.per_warp /= 2;
     const int64_t grid = mx::div_up(rows, 8 * a.per_warp) * a.segments;
     if (grid > INT_MAX) return MX_ERR_UNSUPPORTED;
-#define MX_ROWS(T)                                                                      \
-    (sixteen ? mx::rows_typed<T, true, 16>(x, x_stride, a, block, grid, stream)         \
-     : wide  ? mx::rows_typed<T, true, 8>(x, x_stride, a, block, grid, stream)          \
-             : mx::rows_typed<T, false, 8>(x, x_stride, a, block, grid, stream))
+#define MX_ROWS(T) mx::rows_any<T>(x, x_stride, a, block, grid, in, wide, sixteen, stream)
     if (dtype == MX_F32) return MX_ROWS(float);
     if (dtype == MX_BF16) return MX_ROWS(__nv_bfloat16);
     return MX_ROWS(__half);
@@ -481,7 +500,7 @@ mx_status mx_quantize_cols(const void *x, mx_dtype dtype, int64_t rows, int64_t 
     a.col_tiles = (int32_t)mx::div_up(cols, 128);
     a.tiles = mx_padded_rows(rows, num_groups) / 128 * a.col_tiles;
     a.e5m2 = out_dtype == MX_E5M2;
-    return mx::tiles_any<false>(x, dtype, a, mx::wide_ok(x, x_stride, 0, es, q, q_stride, 0, cols), stream);
+    return mx::tiles_any<false>(x, dtype, a, mx::in_of(x, x_stride, 0, es), mx::wide_of(q, q_stride, 0, 8), stream);
 }
 
 mx_status mx_quantize_blocks(const void *x, mx_dtype dtype, int64_t groups, int64_t rows, int64_t cols, int64_t x_group_stride,
@@ -510,7 +529,7 @@ mx_status mx_quantize_blocks(const void *x, mx_dtype dtype, int64_t groups, int6
     if (mx::div_up(rows, 128) * a.col_tiles > INT64_MAX / mx::kOpsMaxExtent) return MX_ERR_UNSUPPORTED;
     a.tiles = groups * a.row_tiles * a.col_tiles;
     a.e5m2 = out_dtype == MX_E5M2;
-    return mx::tiles_any<true>(x, dtype, a, mx::wide_ok(x, x_stride, a.x_group, es, q, q_stride, a.q_group, cols), stream);
+    return mx::tiles_any<true>(x, dtype, a, mx::in_of(x, x_stride, a.x_group, es), mx::wide_of(q, q_stride, a.q_group, 8), stream);
 }
 
 }  // extern "C"
