@@ -252,3 +252,74 @@ def test_quantize_tiny(mxlib):
     x = torch.tensor([[1e-40, -3e-39, 2.0 ** -149, 0.0], [2.0 ** -126, 2.0 ** -118, -2.0 ** -127, 2.0 ** -119]])
     q, s = mxs.quantize_rows(x.cuda())
     check_quantized(q, s, ref.quantize(x, E4, 1, 128))
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, FL])
+@pytest.mark.parametrize("offset", [1, 2, 3, 4, 8])
+@pytest.mark.parametrize("C,stride", [(37, 45), (64, 80), (129, 130), (530, 544)])
+def test_rows_that_start_anywhere(mxlib, dtype, offset, C, stride):
+    """Inputs and outputs at every alignment give what aligned ones give, and nothing beside them is written."""
+    rng = np.random.default_rng(C + offset)
+    T, k, E = 45, 2, 3
+    order, (ends, row, slot) = order_for(rng, T, k, E)
+
+    def view(rows, fill=None):
+        buf = torch.full((rows * stride + 64,), 77.0, dtype=dtype, device="cuda")
+        v = buf[offset: offset + rows * stride].view(rows, stride)[:, :C]
+        if fill is not None:
+            v.copy_(fill)
+        return buf, v
+
+    x = hard_values(rng, T, C, dtype).cuda()
+    rows = torch.from_numpy(rng.standard_normal((T * k, C))).to(dtype).cuda()
+    w = torch.from_numpy(rng.standard_normal((T, k))).float().cuda()
+    (_, xv), (_, rv) = view(T, x), view(T * k, rows)
+    buf, out = view(T * k)
+    assert torch.equal(mxs.dispatch_rows(xv, order, out=out), mxs.dispatch_rows(x, order))
+    gaps = torch.ones_like(buf, dtype=torch.bool)
+    gaps[offset: offset + T * k * stride].view(T * k, stride)[:, :C] = False
+    assert buf[gaps].eq(77).all()
+    buf, out = view(T)
+    # sums of the same terms in the same order, whatever is loaded at once
+    assert torch.equal(mxs.combine_rows(rv, order, w, out=out), mxs.combine_rows(rows, order, w))
+    gaps = torch.ones_like(buf, dtype=torch.bool)
+    gaps[offset: offset + T * stride].view(T, stride)[:, :C] = False
+    assert buf[gaps].eq(77).all()
+    (a, b), (c, d) = mxs.combine_rows_backward(xv, rv, order, w), mxs.combine_rows_backward(x, rows, order, w)
+    assert torch.equal(a, c)
+    mag = torch.from_numpy(np.stack([[float((x[t].double() * rows[row[t, j]].double()).abs().sum()) if row[t, j] >= 0 else 0.0
+                                      for j in range(k)] for t in range(T)])).cuda()
+    assert ((b - d).double().abs() <= 2 * (C + 1) * 2.0 ** -24 * mag).all()   # sums in another order
+    e = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    for got, want in ((mxs.quantize_rows(xv), mxs.quantize_rows(x)), (mxs.quantize_rows(xv, block=32, order=order), mxs.quantize_rows(x, block=32, order=order)),
+                      (mxs.quantize_cols(rv, e), mxs.quantize_cols(rows, e)), (mxs.quantize_blocks(xv[None]), mxs.quantize_blocks(x[None]))):
+        assert torch.equal(got[0].view(torch.uint8), want[0].view(torch.uint8)) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("offset,stride", [(0, 300), (1, 301), (8, 304), (4, 308)])
+def test_quantized_rows_that_start_anywhere(mxlib, offset, stride):
+    """8-bit outputs at any alignment through the C entry points; the bytes between rows are left alone."""
+    from scale_factor_layout_b200 import _binding as B
+
+    rng = np.random.default_rng(offset)
+    R, C = 70, 299
+    x = hard_values(rng, R, C, BF).cuda()
+    stream = torch.cuda.current_stream().cuda_stream
+    ends = torch.tensor([40, 70], dtype=torch.int32, device="cuda")
+    P = B.mx_padded_rows(R, 2)
+
+    def check(rows, call, want_q, want_s):
+        buf = torch.full((rows * stride + 16,), 0xA5, dtype=torch.uint8, device="cuda")
+        s = torch.zeros(want_s.numel(), dtype=torch.uint8, device="cuda")
+        assert call(buf.data_ptr() + offset, s.data_ptr()) == B.MX_OK
+        torch.cuda.synchronize()
+        body = buf[offset: offset + rows * stride].view(rows, stride)
+        assert torch.equal(body[:, :C], want_q.view(torch.uint8).reshape(rows, C)) and torch.equal(s, want_s.reshape(-1))
+        assert body[:, C:].eq(0xA5).all() and buf[:offset].eq(0xA5).all() and buf[offset + rows * stride:].eq(0xA5).all()
+
+    q, s = mxs.quantize_rows(x)
+    check(R, lambda p, t: B.mx_quantize_rows(x.data_ptr(), B.MX_BF16, R, C, C, 128, B.MX_E4M3, 0, 0, 0, 0, p, stride, t, 1, R, stream), q, s.t().contiguous())
+    q, s = mxs.quantize_cols(x, ends)
+    check(P, lambda p, t: B.mx_quantize_cols(x.data_ptr(), B.MX_BF16, R, C, C, ends.data_ptr(), 2, B.MX_E4M3, p, stride, t, C, stream), q, s)
+    q, s = mxs.quantize_blocks(x[None])
+    check(R, lambda p, t: B.mx_quantize_blocks(x.data_ptr(), B.MX_BF16, 1, R, C, R * C, C, B.MX_E4M3, p, R * stride, stride, t, stream), q, s)
