@@ -207,7 +207,7 @@ int mx_version(void);
  * Strides are in elements.  Outputs must not overlap inputs.  Streams, graphs,
  * contexts and the bounded waits are as described above.  Any alignment and
  * stride is taken; rows that start on 16-byte boundaries are moved 16 bytes at
- * a time, others 4 bytes or one element.  The product alone asks for 16-byte
+ * a time, others 8, 4 or one element's.  The product alone asks for 16-byte
  * aligned operand rows; its contraction is at most 2^25 long, and a row of its
  * output 2^31 - 1 bytes (MX_ERR_UNSUPPORTED). */
 typedef enum { MX_F32 = 0, MX_BF16 = 1, MX_F16 = 2, MX_E4M3 = 3, MX_E5M2 = 4 } mx_dtype;

@@ -167,7 +167,7 @@ sort_place_kernel(const Id *__restrict__ ids, int64_t S, int64_t per_cta, int64_
 // A CTA of 256 threads takes 256 / tpr tokens and one chunk of their rows: kPacks
 // packs a thread, tpr packs apart (tpr a power of two: the packs of a row, at
 // most 256).  Chunks of a token are neighbours in the grid, so their rows are
-// touched together.  A pack is 16 bytes, 4, or one element, whichever all rows
+// touched together.  A pack is 16 bytes, 8, 4, or one element, whichever all rows
 // are aligned to.
 constexpr int kRowThreads = 256;
 
@@ -181,7 +181,7 @@ struct RowShape {
 
 // Packs of a thread that are in flight for each row: enough small loads, and
 // enough of 16 bytes where a token has few rows.
-constexpr int packs_of(int bytes, int ahead) { return bytes == 16 ? 8 / ahead : ahead == 1 ? 4 : ahead == 2 ? 8 : 4; }
+constexpr int packs_of(int bytes, int ahead) { return bytes == 16 ? 8 / ahead : bytes == 8 ? 16 / ahead : ahead == 2 ? 8 : 4; }
 
 template <typename P>
 __device__ __forceinline__ void zero_rows(P *__restrict__ out, int64_t stride, int64_t from, const RowShape &s) {
@@ -205,7 +205,7 @@ __device__ __forceinline__ void place_of(const RowShape &s, int64_t &t, int &p) 
 }
 
 // out[row_of_slot[t, j]] = x[t]; rows from *last_end on = 0.  Strides in packs.
-constexpr int dispatch_packs(int bytes) { return bytes == 16 ? 1 : 4; }
+constexpr int dispatch_packs(int bytes) { return bytes == 16 ? 1 : bytes == 8 ? 2 : bytes == 4 ? 4 : 8; }
 template <typename P>
 __global__ void __launch_bounds__(kRowThreads)
 dispatch_kernel(const P *__restrict__ x, int64_t x_stride, const int *__restrict__ row_of_slot,
@@ -398,12 +398,12 @@ mx_status sort_typed(const void *ids, int64_t S, int32_t E, int32_t *group_ends,
                   static_cast<const int *>(ctas > 1 ? workspace : nullptr), group_ends, row_of_slot, slot_of_row);
 }
 
-// Bytes of a pack: the most of 16 and 4 that every row of every matrix starts on
+// Bytes of a pack: the most of 16, 8 and 4 that every row of every matrix starts on
 // and is made of, else one element's.
 struct Mat { const void *p; int64_t stride; };
 template <int n>
 int pack_bytes(int es, int64_t cols, const Mat (&m)[n]) {
-    for (int bytes : {16, 4}) {
+    for (int bytes : {16, 8, 4}) {
         bool fits = cols * es % bytes == 0;
         for (const Mat &a : m) fits = fits && aligned_to(a.p, bytes) && a.stride * es % bytes == 0;
         if (fits) return bytes;
@@ -507,7 +507,7 @@ mx_status mx_dispatch_rows(const void *x, mx_dtype dtype, int64_t tokens, int64_
     const mx::Mat mats[] = {{x, x_stride}, {out, out_stride}};
 #define MX_DISPATCH(P) mx::dispatch_typed<P>(x, x_stride * es, row_of_slot, last, out, out_stride * es, tokens, choices, cols * es, stream)
     const int bytes = mx::pack_bytes(es, cols, mats);
-    return bytes == 16 ? MX_DISPATCH(uint4) : bytes == 4 ? MX_DISPATCH(uint32_t) : MX_DISPATCH(uint16_t);
+    return bytes == 16 ? MX_DISPATCH(uint4) : bytes == 8 ? MX_DISPATCH(uint2) : bytes == 4 ? MX_DISPATCH(uint32_t) : MX_DISPATCH(uint16_t);
 #undef MX_DISPATCH
 }
 
@@ -526,11 +526,11 @@ mx_status mx_combine_rows(const void *rows, mx_dtype dtype, int64_t tokens, int6
     const mx::Mat mats[] = {{rows, rows_stride}, {y, y_stride}};
     const int bytes = mx::pack_bytes(es, cols, mats);
 #define MX_COMBINE_K(T, N, K) mx::combine_typed<T, N, K>(rows, rows_stride, row_of_slot, weights, y, y_stride, tokens, choices, cols, stream)
-#define MX_COMBINE(T, N) (choices <= 2 ? MX_COMBINE_K(T, N, 2) : MX_COMBINE_K(T, N, 8))
-    if (dtype == MX_F32) return bytes == 16 ? MX_COMBINE(float, 4) : MX_COMBINE(float, 1);
-    if (dtype == MX_BF16)
-        return bytes == 16 ? MX_COMBINE(__nv_bfloat16, 8) : bytes == 4 ? MX_COMBINE(__nv_bfloat16, 2) : MX_COMBINE(__nv_bfloat16, 1);
-    return bytes == 16 ? MX_COMBINE(__half, 8) : bytes == 4 ? MX_COMBINE(__half, 2) : MX_COMBINE(__half, 1);
+#define MX_COMBINE(T, N) (choices <= 2 ? MX_COMBINE_K(T, N, 2) : choices <= 4 ? MX_COMBINE_K(T, N, 4) : MX_COMBINE_K(T, N, 8))
+#define MX_COMBINE_16(T) (bytes == 16 ? MX_COMBINE(T, 8) : bytes == 8 ? MX_COMBINE(T, 4) : bytes == 4 ? MX_COMBINE(T, 2) : MX_COMBINE(T, 1))
+    if (dtype == MX_F32) return bytes == 16 ? MX_COMBINE(float, 4) : bytes == 8 ? MX_COMBINE(float, 2) : MX_COMBINE(float, 1);
+    return dtype == MX_BF16 ? MX_COMBINE_16(__nv_bfloat16) : MX_COMBINE_16(__half);
+#undef MX_COMBINE_16
 #undef MX_COMBINE
 #undef MX_COMBINE_K
 }
@@ -559,11 +559,11 @@ mx_status mx_combine_rows_backward(const void *grad, mx_dtype dtype, int64_t tok
 #define MX_BACKWARD_K(T, N, K)                                                                                            \
     mx::backward_typed<T, N, K>(grad, grad_stride, rows, rows_stride, row_of_slot, last, weights, d_rows, d_rows_stride, \
                                 d_weights, tokens, choices, cols, stream)
-#define MX_BACKWARD(T, N) (choices <= 2 ? MX_BACKWARD_K(T, N, 2) : MX_BACKWARD_K(T, N, 8))
-    if (dtype == MX_F32) return bytes == 16 ? MX_BACKWARD(float, 4) : MX_BACKWARD(float, 1);
-    if (dtype == MX_BF16)
-        return bytes == 16 ? MX_BACKWARD(__nv_bfloat16, 8) : bytes == 4 ? MX_BACKWARD(__nv_bfloat16, 2) : MX_BACKWARD(__nv_bfloat16, 1);
-    return bytes == 16 ? MX_BACKWARD(__half, 8) : bytes == 4 ? MX_BACKWARD(__half, 2) : MX_BACKWARD(__half, 1);
+#define MX_BACKWARD(T, N) (choices <= 2 ? MX_BACKWARD_K(T, N, 2) : choices <= 4 ? MX_BACKWARD_K(T, N, 4) : MX_BACKWARD_K(T, N, 8))
+#define MX_BACKWARD_16(T) (bytes == 16 ? MX_BACKWARD(T, 8) : bytes == 8 ? MX_BACKWARD(T, 4) : bytes == 4 ? MX_BACKWARD(T, 2) : MX_BACKWARD(T, 1))
+    if (dtype == MX_F32) return bytes == 16 ? MX_BACKWARD(float, 4) : bytes == 8 ? MX_BACKWARD(float, 2) : MX_BACKWARD(float, 1);
+    return dtype == MX_BF16 ? MX_BACKWARD_16(__nv_bfloat16) : MX_BACKWARD_16(__half);
+#undef MX_BACKWARD_16
 #undef MX_BACKWARD
 #undef MX_BACKWARD_K
 }

@@ -42,11 +42,12 @@ template <> __device__ __forceinline__ float from_f32<float>(float v) { return v
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
-// N consecutive elements as one load or store moves them: 16 bytes, 4, or one
+// N consecutive elements as one load or store moves them: 16 bytes, 8, 4, or one
 // element, as rows are aligned.  They stay words until they are unpacked: arrays
 // of 16-bit types are not always moved as a whole.
 template <int bytes> struct RawOf;
 template <> struct RawOf<16> { using Type = uint4; };
+template <> struct RawOf<8> { using Type = uint2; };
 template <> struct RawOf<4> { using Type = uint32_t; };
 template <> struct RawOf<2> { using Type = uint16_t; };
 template <typename T, int N> using Raw = typename RawOf<sizeof(T) * N>::Type;
@@ -74,9 +75,14 @@ __device__ __forceinline__ void unpack(const Raw<T, N> &r, float (&f)[N]) {
         f[0] = __uint_as_float(r);
     } else if constexpr (N == 1) {
         f[0] = two_floats<T>(r).x;
+    } else if constexpr (N == 2 && sizeof(T) == 4) {
+        f[0] = __uint_as_float(r.x), f[1] = __uint_as_float(r.y);
     } else if constexpr (N == 2) {
         const float2 a = two_floats<T>(r);
         f[0] = a.x, f[1] = a.y;
+    } else if constexpr (N == 4 && sizeof(T) == 2) {
+        const float2 a = two_floats<T>(r.x), b = two_floats<T>(r.y);
+        f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
     } else if constexpr (sizeof(T) == 4) {
         f[0] = __uint_as_float(r.x), f[1] = __uint_as_float(r.y), f[2] = __uint_as_float(r.z), f[3] = __uint_as_float(r.w);
     } else {
@@ -90,8 +96,12 @@ __device__ __forceinline__ Raw<T, N> pack(const float (&f)[N]) {
         return __float_as_uint(f[0]);
     } else if constexpr (N == 1) {
         return (uint16_t)two_packed<T>(f[0], 0.f);
+    } else if constexpr (N == 2 && sizeof(T) == 4) {
+        return make_uint2(__float_as_uint(f[0]), __float_as_uint(f[1]));
     } else if constexpr (N == 2) {
         return two_packed<T>(f[0], f[1]);
+    } else if constexpr (N == 4 && sizeof(T) == 2) {
+        return make_uint2(two_packed<T>(f[0], f[1]), two_packed<T>(f[2], f[3]));
     } else if constexpr (sizeof(T) == 4) {
         return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
     } else {
