@@ -310,6 +310,12 @@ quantize_tiles_kernel(const T *__restrict__ x, TileArgs a) {
             dst += p * a.q_stride;
             scale_at = rb * a.scale_stride + c0;
         }
+        if (!kSquare && valid <= 0) {   // behind the last group: zeros, and nothing to wait for
+#pragma unroll
+            for (int i = 0; i < 8; ++i) store8<kWide, kIn>(dst + (ty + 16 * i) * a.q_stride, c, a.cols, make_uint2(0u, 0u));
+            if (tid < 128 && c0 + tid < a.cols) a.scales[scale_at + tid] = 0;
+            continue;
+        }
         Eight<T> v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
