@@ -204,8 +204,95 @@ __device__ __forceinline__ void place_of(const RowShape &s, int64_t &t, int &p) 
     p = chunk * (kPacks << s.tpr_log2) + (threadIdx.x & ((1 << s.tpr_log2) - 1));
 }
 
+// Rows of 16-bit elements off 4-byte boundaries.  Loads are of whole words (one that
+// holds a wanted element is always readable), shifted by an element where the row
+// starts between two; stores are of 16 bytes from the row's first boundary on, so
+// that no sector is written in parts but at a row's ends.  48033 tokens x 4 x 2201:
+// 277 us, element by element 393; 29144 x 1 x 2463: 106 and 145.  Rows on 4-byte or
+// 8-byte boundaries are as fast in such packs (48033 x 4 x 2202 and 2204: 263 and
+// 203 us, 315 and 312 this way), and so are combine's reads, which have no stores to gain.
+
+// Elements at .. at + 15 of a row; those past its `cols` are undefined.
+__device__ __forceinline__ void load_sixteen(const uint16_t *row, int at, int cols, uint32_t (&w)[8]) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(row + at);
+    const uint32_t *src = reinterpret_cast<const uint32_t *>(a & ~uintptr_t(3));
+    const int odd = (int)(a >> 1 & 1);
+    uint32_t last = 0;
+    if (at + 16 <= cols) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = __ldg(src + i);
+        if (odd) last = __ldg(src + 8);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = at - odd + 2 * i < cols ? __ldg(src + i) : 0u;
+        if (odd && at + 15 < cols) last = __ldg(src + 8);
+    }
+    if (odd) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = __funnelshift_r(w[i], i < 7 ? w[i + 1] : last, 16);
+    }
+}
+// Eight of them, from element `from` (0..7) on.
+__device__ __forceinline__ uint4 eight_of(const uint32_t (&w)[8], int from) {
+    uint32_t a[6], b[5];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) a[i] = from & 4 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) b[i] = from & 2 ? a[i + 1] : a[i];
+    return from & 1 ? make_uint4(__funnelshift_r(b[0], b[1], 16), __funnelshift_r(b[1], b[2], 16),
+                                 __funnelshift_r(b[2], b[3], 16), __funnelshift_r(b[3], b[4], 16))
+                    : make_uint4(b[0], b[1], b[2], b[3]);
+}
+
+// dispatch_kernel for such rows: a thread holds 15 elements of the token's row at a
+// time, of which each destination takes the eight that it stores as a whole.
+constexpr int kDispatchPieces = 2;
+__global__ void __launch_bounds__(kRowThreads)
+dispatch_elements_kernel(const uint16_t *__restrict__ x, int64_t x_stride, const int *__restrict__ row_of_slot,
+                         const int *__restrict__ last_end, uint16_t *__restrict__ out, int64_t out_stride, int cols, RowShape s) {
+    grid_dependency_wait();
+    int64_t t;
+    int p;
+    place_of<kDispatchPieces>(s, t, p);
+    if (t < s.tokens) {
+        const int tpr = 1 << s.tpr_log2;
+        uint32_t w[kDispatchPieces][8];
+#pragma unroll
+        for (int i = 0; i < kDispatchPieces; ++i)
+            if (p + i * tpr < s.packs) load_sixteen(x + t * x_stride, (p + i * tpr) * 8, cols, w[i]);
+        const int *rows = row_of_slot + t * s.k;
+        for (int j = 0; j < s.k; ++j) {
+            const int64_t r = rows[j];
+            if (r < 0 || r >= s.rows) continue;
+            uint16_t *row = out + r * out_stride;
+            const int first = -(int)(reinterpret_cast<uintptr_t>(row) >> 1) & 7;   // elements before the row's first boundary
+#pragma unroll
+            for (int i = 0; i < kDispatchPieces; ++i) {
+                if (p + i * tpr >= s.packs) break;
+                const int at = (p + i * tpr) * 8 + first;
+                const uint4 v = eight_of(w[i], first);
+                if (at + 8 <= cols) {
+                    *reinterpret_cast<uint4 *>(row + at) = v;
+                } else {
+                    const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        if (at + u < cols) row[at + u] = (uint16_t)(e[u / 2] >> (16 * (u & 1)));
+                }
+                if (at == first) {   // the row's first elements
+#pragma unroll
+                    for (int u = 0; u < 7; ++u)
+                        if (u < first && u < cols) row[u] = (uint16_t)(w[i][u / 2] >> (16 * (u & 1)));
+                }
+            }
+        }
+    }
+    s.packs = cols;
+    zero_rows(out, out_stride, (int64_t)*last_end, s);
+}
+
 // out[row_of_slot[t, j]] = x[t]; rows from *last_end on = 0.  Strides in packs.
-constexpr int dispatch_packs(int bytes) { return bytes == 16 ? 1 : bytes == 8 ? 2 : bytes == 4 ? 4 : 8; }
+constexpr int dispatch_packs(int bytes) { return 16 / bytes; }
 template <typename P>
 __global__ void __launch_bounds__(kRowThreads)
 dispatch_kernel(const P *__restrict__ x, int64_t x_stride, const int *__restrict__ row_of_slot,
@@ -434,6 +521,15 @@ mx_status dispatch_typed(const void *x, int64_t x_bytes, const int32_t *row_of_s
                   last_end, static_cast<P *>(out), out_bytes / n, s);
 }
 
+mx_status dispatch_elements(const void *x, int64_t x_stride, const int32_t *row_of_slot, const int32_t *last_end, void *out,
+                            int64_t out_stride, int64_t tokens, int32_t choices, int64_t cols, cudaStream_t stream) {
+    RowShape s;
+    int64_t grid;
+    if (mx_status st = row_shape(tokens, choices, div_up(cols, 8), kDispatchPieces, &s, &grid); st != MX_OK) return st;
+    return launch(dispatch_elements_kernel, grid, kRowThreads, 0, stream, static_cast<const uint16_t *>(x), x_stride, row_of_slot,
+                  last_end, static_cast<uint16_t *>(out), out_stride, (int)cols, s);
+}
+
 template <typename T, int N, int kAhead>
 mx_status combine_typed(const void *rows, int64_t rows_stride, const int32_t *row_of_slot, const float *weights, void *y,
                         int64_t y_stride, int64_t tokens, int32_t choices, int64_t cols, cudaStream_t stream) {
@@ -505,9 +601,10 @@ mx_status mx_dispatch_rows(const void *x, mx_dtype dtype, int64_t tokens, int64_
     if (mx_status st = mx_device_sms(&sms); st != MX_OK) return st;
     const int32_t *last = group_ends + num_experts - 1;
     const mx::Mat mats[] = {{x, x_stride}, {out, out_stride}};
-#define MX_DISPATCH(P) mx::dispatch_typed<P>(x, x_stride * es, row_of_slot, last, out, out_stride * es, tokens, choices, cols * es, stream)
     const int bytes = mx::pack_bytes(es, cols, mats);
-    return bytes == 16 ? MX_DISPATCH(uint4) : bytes == 8 ? MX_DISPATCH(uint2) : bytes == 4 ? MX_DISPATCH(uint32_t) : MX_DISPATCH(uint16_t);
+    if (bytes == 2) return mx::dispatch_elements(x, x_stride, row_of_slot, last, out, out_stride, tokens, choices, cols, stream);
+#define MX_DISPATCH(P) mx::dispatch_typed<P>(x, x_stride * es, row_of_slot, last, out, out_stride * es, tokens, choices, cols * es, stream)
+    return bytes == 16 ? MX_DISPATCH(uint4) : bytes == 8 ? MX_DISPATCH(uint2) : MX_DISPATCH(uint32_t);
 #undef MX_DISPATCH
 }
 

@@ -13,8 +13,8 @@
 // Everything here is bound by memory.  A thread holds 8 or 16 consecutive
 // elements, because a block of 128 is then 16 or 8 neighbouring lanes and its
 // maximum 4 or 3 shuffles.  On a B200, 131072 x 7168 bf16: rows 411 us (6.85
-// TB/s; 8 elements a lane 522), columns of 8 groups 497 us (5.7 TB/s), 128 x 128
-// blocks 459 us (6.1 TB/s); 16384 tokens to 131072 rows in expert order 217 us
+// TB/s; 8 elements a lane 522), columns of 8 groups 470 us (6.0 TB/s), 128 x 128
+// blocks 455 us (6.2 TB/s); 16384 tokens to 131072 rows in expert order 217 us
 // (5.4 TB/s), 23 of them for the scales, whose bytes go to scattered rows.
 
 #include <climits>
@@ -53,11 +53,12 @@ __device__ __forceinline__ uint2 eight_bytes(const float (&v)[8], bool e5m2) {
 constexpr uint32_t kNanBytes = 0x7f7f7f7fu;   // four NaNs in both types
 
 // Eight consecutive elements of a row from column c on, zeros past `cols`, as
-// the words that hold them.  kIn: rows start on 16-byte boundaries, on 4-byte
-// ones, or anywhere; kWide, of the 8-bit rows, on 8-byte ones.  kWhole: on 16-byte
-// and 8-byte ones, and cols is a multiple of 8: without the code for a rest, tiles
-// of 128 x 128 take 459 us where they take 524 with it.
-enum In { kAnywhere = 0, kWords = 1, kVectors = 2, kWhole = 3 };
+// the words that hold them.  kIn: rows start on 16-byte boundaries, or anywhere;
+// kWide, of the 8-bit rows, on 8-byte ones.  kWhole: on 16-byte and 8-byte ones, and
+// cols is a multiple of 8: without the code for a rest, tiles of 128 x 128 take 455
+// us where they take 523 with it.  Anywhere costs about twice the time of whole
+// rows (48033 x 2201 bf16: rows 85 us, blocks 103; 2202: 79 and 76).
+enum In { kAnywhere = 0, kVectors = 1, kWhole = 2 };
 template <typename T> struct Eight { uint4 q[sizeof(T) / 2]; };
 template <typename T, int kIn>
 __device__ __forceinline__ Eight<T> load8(const T *row, int c, int cols) {
@@ -71,9 +72,17 @@ __device__ __forceinline__ Eight<T> load8(const T *row, int c, int cols) {
     if (kIn == kVectors && c + 8 <= cols) {
 #pragma unroll
         for (int i = 0; i < (int)sizeof(T) / 2; ++i) v.q[i] = __ldg(reinterpret_cast<const uint4 *>(row + c) + i);
-    } else if (kIn == kWords && sizeof(T) == 2 && c + 8 <= cols) {
-        const uint32_t *src = reinterpret_cast<const uint32_t *>(row + c);
+    } else if (sizeof(T) == 2 && c + 8 <= cols) {
+        // off a 4-byte boundary: the five words that hold the elements, each of
+        // which holds at least one
+        const uintptr_t at = reinterpret_cast<uintptr_t>(row + c);
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(at & ~uintptr_t(3));
         v.q[0] = make_uint4(__ldg(src), __ldg(src + 1), __ldg(src + 2), __ldg(src + 3));
+        if (at & 2) {
+            const uint32_t last = __ldg(src + 4);
+            v.q[0] = make_uint4(__funnelshift_r(v.q[0].x, v.q[0].y, 16), __funnelshift_r(v.q[0].y, v.q[0].z, 16),
+                                __funnelshift_r(v.q[0].z, v.q[0].w, 16), __funnelshift_r(v.q[0].w, last, 16));
+        }
     } else {
         using W = Raw<T, 1>;
         const W *src = reinterpret_cast<const W *>(row);
@@ -259,7 +268,7 @@ quantize_rows_kernel(const T *__restrict__ x, int64_t x_stride, RowsArgs a) {
 // columns.  Column blocks (one scale a column) and square blocks (one a tile)
 // differ in how far the maximum is reduced.  Four CTAs an SM (16-bit input, 64
 // registers) overlap one tile's stores with another's loads: with two, columns
-// took 720 us where they take 497.
+// took 720 us where they took 497.
 struct TileArgs {
     int64_t x_stride, x_group;      // elements
     uint8_t *q;
@@ -386,7 +395,7 @@ int in_bytes(mx_dtype t) { return t == MX_F32 ? 4 : t == MX_BF16 || t == MX_F16 
 // How rows of the input are aligned, and whether those of the output are.
 int in_of(const void *x, int64_t x_stride, int64_t x_group, int es) {
     const auto on = [&](int64_t n) { return aligned_to(x, n) && x_stride * es % n == 0 && x_group * es % n == 0; };
-    return on(16) ? kVectors : es == 2 && on(4) ? kWords : kAnywhere;
+    return on(16) ? kVectors : kAnywhere;
 }
 bool wide_of(const void *q, int64_t q_stride, int64_t q_group, int64_t n) {
     return aligned_to(q, n) && q_stride % n == 0 && q_group % n == 0;
@@ -410,8 +419,6 @@ mx_status rows_any(const void *x, int64_t x_stride, const RowsArgs &a, int block
     if (sixteen) return rows_typed<T, kWhole, true, 16>(x, x_stride, a, block, grid, stream);
     if (!wide) return rows_typed<T, kAnywhere, false, 8>(x, x_stride, a, block, grid, stream);
     if (in == kVectors) return rows_typed<T, kVectors, true, 8>(x, x_stride, a, block, grid, stream);
-    if constexpr (sizeof(T) == 2)
-        if (in == kWords) return rows_typed<T, kWords, true, 8>(x, x_stride, a, block, grid, stream);
     return rows_typed<T, kAnywhere, true, 8>(x, x_stride, a, block, grid, stream);
 }
 
@@ -426,8 +433,6 @@ mx_status tiles_typed(const void *x, const TileArgs &a, int in, bool wide, cudaS
         return launch(quantize_tiles_kernel<T, kWhole, true, kSquare>, grid, kQThreads, 0, stream, p, a);
     if (!wide) return launch(quantize_tiles_kernel<T, kAnywhere, false, kSquare>, grid, kQThreads, 0, stream, p, a);
     if (in == kVectors) return launch(quantize_tiles_kernel<T, kVectors, true, kSquare>, grid, kQThreads, 0, stream, p, a);
-    if constexpr (sizeof(T) == 2)
-        if (in == kWords) return launch(quantize_tiles_kernel<T, kWords, true, kSquare>, grid, kQThreads, 0, stream, p, a);
     return launch(quantize_tiles_kernel<T, kAnywhere, true, kSquare>, grid, kQThreads, 0, stream, p, a);
 }
 

@@ -323,3 +323,27 @@ def test_quantized_rows_that_start_anywhere(mxlib, offset, stride):
     check(P, lambda p, t: B.mx_quantize_cols(x.data_ptr(), B.MX_BF16, R, C, C, ends.data_ptr(), 2, B.MX_E4M3, p, stride, t, C, stream), q, s)
     q, s = mxs.quantize_blocks(x[None])
     check(R, lambda p, t: B.mx_quantize_blocks(x.data_ptr(), B.MX_BF16, 1, R, C, R * C, C, B.MX_E4M3, p, R * stride, stride, t, stream), q, s)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("C", [1, 2, 3, 6, 7, 8, 9, 15, 16, 17, 23, 31, 257, 4095, 4097, 8231])
+@pytest.mark.parametrize("k", [1, 3])
+def test_dispatch_of_odd_strides(mxlib, dtype, C, k):
+    """Each row starts at another alignment, in the tokens and in expert order: the same bits arrive, and no gap is written."""
+    rng = np.random.default_rng(C + k)
+    T, E = 19, 4
+    order, (ends, row, slot) = order_for(rng, T, k, E)
+    bits = torch.from_numpy(rng.integers(-32768, 32768, size=(T, C + C % 2 + 3)).astype(np.int16))
+    x = bits.cuda().view(dtype)[:, 1:C + 1]
+    stride = C + 5 + C % 2
+    buf = torch.full((T * k * stride + 8,), 77, dtype=torch.int16, device="cuda")
+    out = buf[3: 3 + T * k * stride].view(T * k, stride)[:, :C]
+    mxs.dispatch_rows(x, order, out=out.view(dtype))
+    want = torch.full((T * k * stride + 8,), 77, dtype=torch.int16)
+    inner = want[3: 3 + T * k * stride].view(T * k, stride)
+    inner[:, :C] = 0
+    for t in range(T):
+        for j in range(k):
+            if row[t, j] >= 0:
+                inner[row[t, j], :C] = bits[t, 1:C + 1]
+    assert torch.equal(buf.cpu(), want)
