@@ -204,13 +204,12 @@ __device__ __forceinline__ void place_of(const RowShape &s, int64_t &t, int &p) 
     p = chunk * (kPacks << s.tpr_log2) + (threadIdx.x & ((1 << s.tpr_log2) - 1));
 }
 
-// Rows of 16-bit elements off 4-byte boundaries.  Loads are of whole words (one that
-// holds a wanted element is always readable), shifted by an element where the row
-// starts between two; stores are of 16 bytes from the row's first boundary on, so
-// that no sector is written in parts but at a row's ends.  48033 tokens x 4 x 2201:
-// 277 us, element by element 393; 29144 x 1 x 2463: 106 and 145.  Rows on 4-byte or
-// 8-byte boundaries are as fast in such packs (48033 x 4 x 2202 and 2204: 263 and
-// 203 us, 315 and 312 this way), and so are combine's reads, which have no stores to gain.
+// Rows off 8-byte boundaries, as elements of 16 bits (32-bit ones are two).  Loads
+// are of whole words (one that holds a wanted element is always readable), shifted
+// by an element where the row starts between two; stores are of 16 bytes from the
+// row's first boundary on, so that no sector is written in parts but at a row's
+// ends.  48033 tokens x 4 x 2201 bf16: 235 us, element by element 393; 2202, 4-byte
+// boundaries: 228, in packs of 4 bytes 260; 29144 x 1 x 2463: 87 and 145.
 
 // Elements at .. at + 15 of a row; those past its `cols` are undefined.
 __device__ __forceinline__ void load_sixteen(const uint16_t *row, int at, int cols, uint32_t (&w)[8]) {
@@ -247,6 +246,7 @@ __device__ __forceinline__ uint4 eight_of(const uint32_t (&w)[8], int from) {
 // dispatch_kernel for such rows: a thread holds 15 elements of the token's row at a
 // time, of which each destination takes the eight that it stores as a whole.
 constexpr int kDispatchPieces = 2;
+template <typename P>
 __global__ void __launch_bounds__(kRowThreads)
 dispatch_elements_kernel(const uint16_t *__restrict__ x, int64_t x_stride, const int *__restrict__ row_of_slot,
                          const int *__restrict__ last_end, uint16_t *__restrict__ out, int64_t out_stride, int cols, RowShape s) {
@@ -287,8 +287,9 @@ dispatch_elements_kernel(const uint16_t *__restrict__ x, int64_t x_stride, const
             }
         }
     }
-    s.packs = cols;
-    zero_rows(out, out_stride, (int64_t)*last_end, s);
+    constexpr int kOfPack = sizeof(P) / 2;
+    s.packs = cols / kOfPack;
+    zero_rows(reinterpret_cast<P *>(out), out_stride / kOfPack, (int64_t)*last_end, s);
 }
 
 // out[row_of_slot[t, j]] = x[t]; rows from *last_end on = 0.  Strides in packs.
@@ -521,13 +522,15 @@ mx_status dispatch_typed(const void *x, int64_t x_bytes, const int32_t *row_of_s
                   last_end, static_cast<P *>(out), out_bytes / n, s);
 }
 
-mx_status dispatch_elements(const void *x, int64_t x_stride, const int32_t *row_of_slot, const int32_t *last_end, void *out,
-                            int64_t out_stride, int64_t tokens, int32_t choices, int64_t cols, cudaStream_t stream) {
+template <typename P>
+mx_status dispatch_elements(const void *x, int64_t x_bytes, const int32_t *row_of_slot, const int32_t *last_end, void *out,
+                            int64_t out_bytes, int64_t tokens, int32_t choices, int64_t row_bytes, cudaStream_t stream) {
     RowShape s;
     int64_t grid;
-    if (mx_status st = row_shape(tokens, choices, div_up(cols, 8), kDispatchPieces, &s, &grid); st != MX_OK) return st;
-    return launch(dispatch_elements_kernel, grid, kRowThreads, 0, stream, static_cast<const uint16_t *>(x), x_stride, row_of_slot,
-                  last_end, static_cast<uint16_t *>(out), out_stride, (int)cols, s);
+    if (row_bytes / 2 > kOpsMaxExtent) return MX_ERR_UNSUPPORTED;
+    if (mx_status st = row_shape(tokens, choices, div_up(row_bytes, 16), kDispatchPieces, &s, &grid); st != MX_OK) return st;
+    return launch(dispatch_elements_kernel<P>, grid, kRowThreads, 0, stream, static_cast<const uint16_t *>(x), x_bytes / 2, row_of_slot,
+                  last_end, static_cast<uint16_t *>(out), out_bytes / 2, (int)(row_bytes / 2), s);
 }
 
 template <typename T, int N, int kAhead>
@@ -602,9 +605,11 @@ mx_status mx_dispatch_rows(const void *x, mx_dtype dtype, int64_t tokens, int64_
     const int32_t *last = group_ends + num_experts - 1;
     const mx::Mat mats[] = {{x, x_stride}, {out, out_stride}};
     const int bytes = mx::pack_bytes(es, cols, mats);
-    if (bytes == 2) return mx::dispatch_elements(x, x_stride, row_of_slot, last, out, out_stride, tokens, choices, cols, stream);
-#define MX_DISPATCH(P) mx::dispatch_typed<P>(x, x_stride * es, row_of_slot, last, out, out_stride * es, tokens, choices, cols * es, stream)
-    return bytes == 16 ? MX_DISPATCH(uint4) : bytes == 8 ? MX_DISPATCH(uint2) : MX_DISPATCH(uint32_t);
+#define MX_DISPATCH(F, P) mx::F<P>(x, x_stride * es, row_of_slot, last, out, out_stride * es, tokens, choices, cols * es, stream)
+    return bytes == 16  ? MX_DISPATCH(dispatch_typed, uint4)
+           : bytes == 8 ? MX_DISPATCH(dispatch_typed, uint2)
+           : bytes == 4 ? MX_DISPATCH(dispatch_elements, uint32_t)
+                        : MX_DISPATCH(dispatch_elements, uint16_t);
 #undef MX_DISPATCH
 }
 
