@@ -227,7 +227,8 @@ mx_status mx_expert_sort(const void *expert_ids, int32_t id_bytes, int64_t token
                          cudaStream_t stream);
 
 /* out[row_of_slot[t, j]] = x[t] for tokens * choices rows of out (f32, bf16 or
- * f16).  Its gradient is mx_combine_rows without weights. */
+ * f16).  Its gradient is mx_combine_rows without weights.  Rows off 8-byte boundaries
+ * have less than 2^32 - 2^15 bytes (MX_ERR_UNSUPPORTED). */
 mx_status mx_dispatch_rows(const void *x, mx_dtype dtype, int64_t tokens, int64_t cols, int64_t x_stride,
                            const int32_t *row_of_slot, int32_t choices, const int32_t *group_ends, int32_t num_experts,
                            void *out, int64_t out_stride, cudaStream_t stream);

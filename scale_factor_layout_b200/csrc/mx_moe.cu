@@ -527,7 +527,6 @@ mx_status dispatch_elements(const void *x, int64_t x_bytes, const int32_t *row_o
                             int64_t out_bytes, int64_t tokens, int32_t choices, int64_t row_bytes, cudaStream_t stream) {
     RowShape s;
     int64_t grid;
-    if (row_bytes / 2 > kOpsMaxExtent) return MX_ERR_UNSUPPORTED;
     if (mx_status st = row_shape(tokens, choices, div_up(row_bytes, 16), kDispatchPieces, &s, &grid); st != MX_OK) return st;
     return launch(dispatch_elements_kernel<P>, grid, kRowThreads, 0, stream, static_cast<const uint16_t *>(x), x_bytes / 2, row_of_slot,
                   last_end, static_cast<uint16_t *>(out), out_bytes / 2, (int)(row_bytes / 2), s);
@@ -600,11 +599,12 @@ mx_status mx_dispatch_rows(const void *x, mx_dtype dtype, int64_t tokens, int64_
     if (x == nullptr || out == nullptr || row_of_slot == nullptr || group_ends == nullptr) return MX_ERR_INVALID_ARG;
     if (!mx::aligned_to(x, es) || !mx::aligned_to(out, es) || !mx::aligned_to(row_of_slot, 4) || !mx::aligned_to(group_ends, 4))
         return MX_ERR_MISALIGNED;
+    const mx::Mat mats[] = {{x, x_stride}, {out, out_stride}};
+    const int bytes = mx::pack_bytes(es, cols, mats);
+    if (bytes < 8 && cols * es / 2 > mx::kOpsMaxExtent) return MX_ERR_UNSUPPORTED;
     int sms = 0;
     if (mx_status st = mx_device_sms(&sms); st != MX_OK) return st;
     const int32_t *last = group_ends + num_experts - 1;
-    const mx::Mat mats[] = {{x, x_stride}, {out, out_stride}};
-    const int bytes = mx::pack_bytes(es, cols, mats);
 #define MX_DISPATCH(F, P) mx::F<P>(x, x_stride * es, row_of_slot, last, out, out_stride * es, tokens, choices, cols * es, stream)
     return bytes == 16  ? MX_DISPATCH(dispatch_typed, uint4)
            : bytes == 8 ? MX_DISPATCH(dispatch_typed, uint2)

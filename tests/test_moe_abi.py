@@ -166,3 +166,9 @@ def test_wrappers_refuse():
     refuse(mxs.grouped_matmul, a, s, b, s, ends, out_dtype=torch.float64, match="out_dtype")
     refuse(mxs.grouped_matmul_k, f8(128, 8), u8(1, 8), f8(128, 8), u8(1, 8), ends, match="CUDA")
     refuse(mxs.grouped_matmul_k, f8(128, 8), u8(1, 8), f8(128, 8), u8(1, 8), ends, out_dtype=torch.int8, match="out_dtype")
+
+
+def test_rows_too_long_off_8_byte_boundaries():
+    """Such rows are indexed by halves of 16 bits, in 31 bits."""
+    n = 2**30 + 1
+    assert call("mx_dispatch_rows", DISPATCH, dtype=B.MX_F32, tokens=1, cols=n, x_stride=n, out_stride=n) == UNSUPPORTED
