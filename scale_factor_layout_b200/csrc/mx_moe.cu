@@ -154,7 +154,8 @@ sort_place_kernel(const Id *__restrict__ ids, int64_t S, int64_t per_cta, int64_
         __syncwarp();
         if (at + lane < to) {
             row_of_slot[at + lane] = row;
-            if (row >= 0) slot_of_row[row] = (int)(at + lane);
+            // below S unless the ids or the workspace changed since they were counted
+            if (row >= 0 && row < S) slot_of_row[row] = (int)(at + lane);
         }
     }
     // rows behind the last group

@@ -139,9 +139,11 @@ def expert_sort(expert_ids: torch.Tensor, num_experts: int) -> ExpertOrder:
     row_of_slot = torch.empty_strided((T, k), (k, 1), dtype=i32, device=dev)
     slot_of_row = torch.empty_strided((S,), (1,), dtype=i32, device=dev)
     need = _sort_workspace(T, k)
-    workspace = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=dev).data_ptr() if need else 0
+    # held until both kernels are on the stream: from then on whoever gets this memory on the same stream comes after
+    # them, but a thread that shares the stream could be given it between them
+    workspace = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=dev) if need else None
     _call("mx_expert_sort", dev, expert_ids.data_ptr(), 4 if expert_ids.dtype == i32 else 8, T, k, num_experts,
-          ends.data_ptr(), row_of_slot.data_ptr(), slot_of_row.data_ptr(), workspace)
+          ends.data_ptr(), row_of_slot.data_ptr(), slot_of_row.data_ptr(), workspace.data_ptr() if need else 0)
     return ExpertOrder(ends, row_of_slot, slot_of_row)
 
 
