@@ -204,7 +204,7 @@ int mx_version(void);
  * are written as zeros.  Indexes in device memory that are out of range are
  * skipped, never followed.
  *
- * Strides are in elements.  Outputs must not overlap inputs.  Streams, graphs,
+ * Strides are in elements, and below 2^40 bytes (MX_ERR_UNSUPPORTED).  Outputs must not overlap inputs.  Streams, graphs,
  * contexts and the bounded waits are as described above.  Any alignment and
  * stride is taken; rows that start on 16-byte boundaries are moved 16 bytes at
  * a time, others 8, 4 or one element's.  The product alone asks for 16-byte

@@ -857,8 +857,6 @@ mx_status launch_planned(const Plan &p, const Maps &maps, const MatArgs &a, cuda
                     : launch_product<kForm, kScales, 256, kAlone>(maps, a, 1, stream);
 }
 
-constexpr int64_t kMaxStride = 1ll << 40;   // what a tensor map can hold
-
 bool operand_ok(const void *p, int64_t stride) { return aligned_to(p, 16) && stride % 16 == 0; }
 
 }  // namespace
@@ -889,14 +887,15 @@ mx_status mx_grouped_matmul_m(const void *a, mx_dtype a_dtype, int64_t a_stride,
     if (rows > kOpsMaxExtent || n > kOpsMaxExtent || k > kOpsMaxExtent) return MX_ERR_INVALID_ARG;
     const bool nk = b_layout == MX_B_NK;
     if (a_stride < k || b_stride < (nk ? k : n) || out_stride < n) return MX_ERR_INVALID_ARG;
-    if (a_stride >= kMaxStride || b_stride >= kMaxStride || b_group_stride >= kMaxStride || out_stride >= kMaxStride)
+    const int os = out_dtype == MX_F32 ? 4 : 2;
+    if (!stride_fits(a_stride, 1) || !stride_fits(b_stride, 1) || (num_groups > 1 && !stride_fits(b_group_stride, 1)) ||
+        !stride_fits(out_stride, os))
         return MX_ERR_UNSUPPORTED;
-    if (num_groups > 1 && b_group_stride < b_stride * ((nk ? n : k) - 1) + (nk ? k : n)) return MX_ERR_INVALID_ARG;
+    if (num_groups > 1 && !rows_fit(nk ? n : k, b_stride, nk ? k : n, b_group_stride)) return MX_ERR_INVALID_ARG;
     if (block == 32 && !nk) return MX_ERR_UNSUPPORTED;
     if (rows == 0 || n == 0) return MX_OK;
     if (a == nullptr || b == nullptr || a_scales == nullptr || b_scales == nullptr || group_ends == nullptr || out == nullptr)
         return MX_ERR_INVALID_ARG;
-    const int os = out_dtype == MX_F32 ? 4 : 2;
     if (!operand_ok(a, a_stride) || !operand_ok(b, b_stride) || (num_groups > 1 && b_group_stride % 16 != 0) ||
         !aligned_to(out, os) || !aligned_to(group_ends, 4))
         return MX_ERR_MISALIGNED;
@@ -956,13 +955,14 @@ mx_status mx_grouped_matmul_k(const void *a, mx_dtype a_dtype, int64_t a_stride,
         return MX_ERR_INVALID_ARG;
     if (padded_rows > kOpsMaxExtent || m > kOpsMaxExtent || n > kOpsMaxExtent) return MX_ERR_INVALID_ARG;
     if (a_stride < m || b_stride < n || a_scale_stride < m || b_scale_stride < n || out_stride < n) return MX_ERR_INVALID_ARG;
-    if (a_stride >= kMaxStride || b_stride >= kMaxStride || out_stride >= kMaxStride || out_group_stride >= kMaxStride)
+    const int os = out_dtype == MX_F32 ? 4 : 2;
+    if (!stride_fits(a_stride, 1) || !stride_fits(b_stride, 1) || !stride_fits(out_stride, os) ||
+        (num_groups > 1 && !stride_fits(out_group_stride, os)))
         return MX_ERR_UNSUPPORTED;
-    if (num_groups > 1 && m > 0 && out_group_stride < (m - 1) * out_stride + n) return MX_ERR_INVALID_ARG;
+    if (num_groups > 1 && !rows_fit(m, out_stride, n, out_group_stride)) return MX_ERR_INVALID_ARG;
     if (m == 0 || n == 0) return MX_OK;
     if (a == nullptr || b == nullptr || a_scales == nullptr || b_scales == nullptr || group_ends == nullptr || out == nullptr)
         return MX_ERR_INVALID_ARG;
-    const int os = out_dtype == MX_F32 ? 4 : 2;
     if (!operand_ok(a, a_stride) || !operand_ok(b, b_stride) || !aligned_to(out, os) || !aligned_to(group_ends, 4))
         return MX_ERR_MISALIGNED;
 

@@ -596,6 +596,7 @@ mx_status mx_dispatch_rows(const void *x, mx_dtype dtype, int64_t tokens, int64_
     const int es = mx::element_bytes(dtype);
     if (es == 0 || !mx::slots_ok(tokens, choices) || cols < 0 || cols > mx::kOpsMaxExtent) return MX_ERR_INVALID_ARG;
     if (num_experts < 1 || num_experts > MX_MAX_GROUPS || x_stride < cols || out_stride < cols) return MX_ERR_INVALID_ARG;
+    if (!mx::stride_fits(x_stride, es) || !mx::stride_fits(out_stride, es)) return MX_ERR_UNSUPPORTED;
     if (tokens == 0 || cols == 0) return MX_OK;
     if (x == nullptr || out == nullptr || row_of_slot == nullptr || group_ends == nullptr) return MX_ERR_INVALID_ARG;
     if (!mx::aligned_to(x, es) || !mx::aligned_to(out, es) || !mx::aligned_to(row_of_slot, 4) || !mx::aligned_to(group_ends, 4))
@@ -620,6 +621,7 @@ mx_status mx_combine_rows(const void *rows, mx_dtype dtype, int64_t tokens, int6
     const int es = mx::element_bytes(dtype);
     if (es == 0 || !mx::slots_ok(tokens, choices) || cols < 0 || cols > mx::kOpsMaxExtent) return MX_ERR_INVALID_ARG;
     if (rows_stride < cols || y_stride < cols) return MX_ERR_INVALID_ARG;
+    if (!mx::stride_fits(rows_stride, es) || !mx::stride_fits(y_stride, es)) return MX_ERR_UNSUPPORTED;
     if (tokens == 0 || cols == 0) return MX_OK;
     if (rows == nullptr || y == nullptr || row_of_slot == nullptr) return MX_ERR_INVALID_ARG;
     if (!mx::aligned_to(rows, es) || !mx::aligned_to(y, es) || !mx::aligned_to(row_of_slot, 4) || !mx::aligned_to(weights, 4))
@@ -646,6 +648,8 @@ mx_status mx_combine_rows_backward(const void *grad, mx_dtype dtype, int64_t tok
     if (es == 0 || !mx::slots_ok(tokens, choices) || cols < 1 || cols > mx::kOpsMaxExtent) return MX_ERR_INVALID_ARG;
     if (num_experts < 1 || num_experts > MX_MAX_GROUPS) return MX_ERR_INVALID_ARG;
     if (grad_stride < cols || rows_stride < cols || d_rows_stride < cols) return MX_ERR_INVALID_ARG;
+    if (!mx::stride_fits(grad_stride, es) || !mx::stride_fits(rows_stride, es) || !mx::stride_fits(d_rows_stride, es))
+        return MX_ERR_UNSUPPORTED;
     if (tokens == 0) return MX_OK;
     if (grad == nullptr || rows == nullptr || row_of_slot == nullptr || group_ends == nullptr || weights == nullptr ||
         d_rows == nullptr || d_weights == nullptr)

@@ -22,6 +22,13 @@ constexpr int64_t kOpsMaxExtent = (1ll << 31) - (1ll << 14);
 
 inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int64_t up_to(int64_t a, int64_t b) { return div_up(a, b) * b; }
+// Strides are below 2^40 bytes: what a tensor map can hold, more than any memory has,
+// and few enough that the host's arithmetic on them stays within 64 bits.
+inline bool stride_fits(int64_t stride, int64_t element_bytes) { return stride < (1ll << 40) / element_bytes; }
+// Whether rows of `cols` elements, `stride` apart, lie within `room` elements.
+inline bool rows_fit(int64_t rows, int64_t stride, int64_t cols, int64_t room) {
+    return rows < 1 || (cols <= room && (stride < 1 || rows - 1 <= (room - cols) / stride));
+}
 inline bool aligned_to(const void *p, int64_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 // A stream-ordered launch whose own return code is the result (the thread's

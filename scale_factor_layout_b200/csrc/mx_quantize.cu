@@ -458,6 +458,9 @@ mx_status mx_quantize_rows(const void *x, mx_dtype dtype, int64_t rows, int64_t 
     if (es == 0 || !mx::eight_bit_type(out_dtype) || (block != 128 && block != 32)) return MX_ERR_INVALID_ARG;
     if (rows < 0 || cols < 0 || rows > mx::kOpsMaxExtent || cols > mx::kOpsMaxExtent) return MX_ERR_INVALID_ARG;
     if (x_stride < cols || q_stride < cols || scale_row_stride < 1 || scale_block_stride < 1) return MX_ERR_INVALID_ARG;
+    if (!mx::stride_fits(x_stride, es) || !mx::stride_fits(q_stride, 1) || !mx::stride_fits(scale_row_stride, 1) ||
+        !mx::stride_fits(scale_block_stride, 1))
+        return MX_ERR_UNSUPPORTED;
     const bool order = row_of_slot != nullptr;
     if (order && (choices < 1 || rows * choices > mx::kOpsMaxExtent || num_experts < 1 || num_experts > MX_MAX_GROUPS ||
                   group_ends == nullptr))
@@ -507,6 +510,8 @@ mx_status mx_quantize_cols(const void *x, mx_dtype dtype, int64_t rows, int64_t 
     if (es == 0 || !mx::eight_bit_type(out_dtype) || num_groups < 1 || num_groups > MX_MAX_GROUPS) return MX_ERR_INVALID_ARG;
     if (rows < 0 || cols < 0 || rows > mx::kOpsMaxExtent || cols > mx::kOpsMaxExtent) return MX_ERR_INVALID_ARG;
     if (x_stride < cols || q_stride < cols || scale_stride < cols) return MX_ERR_INVALID_ARG;
+    if (!mx::stride_fits(x_stride, es) || !mx::stride_fits(q_stride, 1) || !mx::stride_fits(scale_stride, 1))
+        return MX_ERR_UNSUPPORTED;
     if (cols == 0) return MX_OK;
     if ((rows > 0 && x == nullptr) || q == nullptr || scales == nullptr || group_ends == nullptr) return MX_ERR_INVALID_ARG;
     if (!mx::aligned_to(x, es) || !mx::aligned_to(group_ends, 4)) return MX_ERR_MISALIGNED;
@@ -534,9 +539,12 @@ mx_status mx_quantize_blocks(const void *x, mx_dtype dtype, int64_t groups, int6
     if (groups < 0 || rows < 0 || cols < 0 || groups > mx::kOpsMaxExtent || rows > mx::kOpsMaxExtent || cols > mx::kOpsMaxExtent)
         return MX_ERR_INVALID_ARG;
     if (x_stride < cols || q_stride < cols || x_group_stride < 0 || q_group_stride < 0) return MX_ERR_INVALID_ARG;
+    if (!mx::stride_fits(x_stride, es) || !mx::stride_fits(q_stride, 1) ||
+        (groups > 1 && (!mx::stride_fits(x_group_stride, es) || !mx::stride_fits(q_group_stride, 1))))
+        return MX_ERR_UNSUPPORTED;
     if (groups == 0 || rows == 0 || cols == 0) return MX_OK;
     if (x == nullptr || q == nullptr || scales == nullptr) return MX_ERR_INVALID_ARG;
-    if (groups > 1 && q_group_stride < (rows - 1) * q_stride + cols) return MX_ERR_INVALID_ARG;
+    if (groups > 1 && !mx::rows_fit(rows, q_stride, cols, q_group_stride)) return MX_ERR_INVALID_ARG;
     if (!mx::aligned_to(x, es)) return MX_ERR_MISALIGNED;
     mx::TileArgs a = {};
     a.x_stride = x_stride;
