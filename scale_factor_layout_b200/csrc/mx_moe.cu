@@ -186,7 +186,6 @@ constexpr int packs_of(int bytes, int ahead) { return bytes == 16 ? 8 / ahead : 
 
 template <typename P>
 __device__ __forceinline__ void zero_rows(P *__restrict__ out, int64_t stride, int64_t from, const RowShape &s) {
-    if (from < 0) from = 0;
     const int64_t n = (s.rows - from) * s.packs;
     P zero;
     memset(&zero, 0, sizeof(zero));
@@ -250,7 +249,7 @@ constexpr int kDispatchPieces = 2;
 template <typename P>
 __global__ void __launch_bounds__(kRowThreads)
 dispatch_elements_kernel(const uint16_t *__restrict__ x, int64_t x_stride, const int *__restrict__ row_of_slot,
-                         const int *__restrict__ last_end, uint16_t *__restrict__ out, int64_t out_stride, int cols, RowShape s) {
+                         const int *__restrict__ ends, int E, uint16_t *__restrict__ out, int64_t out_stride, int cols, RowShape s) {
     grid_dependency_wait();
     int64_t t;
     int p;
@@ -290,15 +289,15 @@ dispatch_elements_kernel(const uint16_t *__restrict__ x, int64_t x_stride, const
     }
     constexpr int kOfPack = sizeof(P) / 2;
     s.packs = cols / kOfPack;
-    zero_rows(reinterpret_cast<P *>(out), out_stride / kOfPack, (int64_t)*last_end, s);
+    zero_rows(reinterpret_cast<P *>(out), out_stride / kOfPack, rows_in_groups(ends, E), s);
 }
 
-// out[row_of_slot[t, j]] = x[t]; rows from *last_end on = 0.  Strides in packs.
+// out[row_of_slot[t, j]] = x[t]; rows behind the last group = 0.  Strides in packs.
 constexpr int dispatch_packs(int bytes) { return 16 / bytes; }
 template <typename P>
 __global__ void __launch_bounds__(kRowThreads)
 dispatch_kernel(const P *__restrict__ x, int64_t x_stride, const int *__restrict__ row_of_slot,
-                const int *__restrict__ last_end, P *__restrict__ out, int64_t out_stride, RowShape s) {
+                const int *__restrict__ ends, int E, P *__restrict__ out, int64_t out_stride, RowShape s) {
     constexpr int kPacks = dispatch_packs(sizeof(P));
     grid_dependency_wait();
     int64_t t;
@@ -319,7 +318,7 @@ dispatch_kernel(const P *__restrict__ x, int64_t x_stride, const int *__restrict
                 if (p + i * tpr < s.packs) out[r * out_stride + p + i * tpr] = v[i];
         }
     }
-    zero_rows(out, out_stride, (int64_t)*last_end, s);
+    zero_rows(out, out_stride, rows_in_groups(ends, E), s);
 }
 
 // y[t] = sum_j w[t, j] * rows[row_of_slot[t, j]] over the slots that have a row;
@@ -377,7 +376,7 @@ combine_kernel(const Raw<T, N> *__restrict__ rows, int64_t rows_stride, const in
 template <typename T, int N, int kTpt, int kAhead>
 __global__ void __launch_bounds__(kRowThreads)
 combine_backward_kernel(const Raw<T, N> *__restrict__ grad, int64_t grad_stride, const Raw<T, N> *__restrict__ rows,
-                        int64_t rows_stride, const int *__restrict__ row_of_slot, const int *__restrict__ last_end,
+                        int64_t rows_stride, const int *__restrict__ row_of_slot, const int *__restrict__ ends, int E,
                         const float *__restrict__ weights, Raw<T, N> *__restrict__ d_rows, int64_t d_rows_stride,
                         float *__restrict__ d_weights, RowShape s) {
     using P = Raw<T, N>;
@@ -454,7 +453,7 @@ combine_backward_kernel(const Raw<T, N> *__restrict__ grad, int64_t grad_stride,
             }
         }
     }
-    zero_rows(d_rows, d_rows_stride, (int64_t)*last_end, s);
+    zero_rows(d_rows, d_rows_stride, rows_in_groups(ends, E), s);
 }
 
 // ------------------------------------------------------------------ host side
@@ -513,24 +512,24 @@ mx_status row_shape(int64_t tokens, int32_t choices, int64_t packs, int per_thre
 }
 
 template <typename P>
-mx_status dispatch_typed(const void *x, int64_t x_bytes, const int32_t *row_of_slot, const int32_t *last_end, void *out,
+mx_status dispatch_typed(const void *x, int64_t x_bytes, const int32_t *row_of_slot, const int32_t *ends, int E, void *out,
                          int64_t out_bytes, int64_t tokens, int32_t choices, int64_t row_bytes, cudaStream_t stream) {
     constexpr int64_t n = sizeof(P);
     RowShape s;
     int64_t grid;
     if (mx_status st = row_shape(tokens, choices, row_bytes / n, dispatch_packs(n), &s, &grid); st != MX_OK) return st;
     return launch(dispatch_kernel<P>, grid, kRowThreads, 0, stream, static_cast<const P *>(x), x_bytes / n, row_of_slot,
-                  last_end, static_cast<P *>(out), out_bytes / n, s);
+                  ends, E, static_cast<P *>(out), out_bytes / n, s);
 }
 
 template <typename P>
-mx_status dispatch_elements(const void *x, int64_t x_bytes, const int32_t *row_of_slot, const int32_t *last_end, void *out,
+mx_status dispatch_elements(const void *x, int64_t x_bytes, const int32_t *row_of_slot, const int32_t *ends, int E, void *out,
                             int64_t out_bytes, int64_t tokens, int32_t choices, int64_t row_bytes, cudaStream_t stream) {
     RowShape s;
     int64_t grid;
     if (mx_status st = row_shape(tokens, choices, div_up(row_bytes, 16), kDispatchPieces, &s, &grid); st != MX_OK) return st;
     return launch(dispatch_elements_kernel<P>, grid, kRowThreads, 0, stream, static_cast<const uint16_t *>(x), x_bytes / 2, row_of_slot,
-                  last_end, static_cast<uint16_t *>(out), out_bytes / 2, (int)(row_bytes / 2), s);
+                  ends, E, static_cast<uint16_t *>(out), out_bytes / 2, (int)(row_bytes / 2), s);
 }
 
 template <typename T, int N, int kAhead>
@@ -546,7 +545,7 @@ mx_status combine_typed(const void *rows, int64_t rows_stride, const int32_t *ro
 
 template <typename T, int N, int kAhead>
 mx_status backward_typed(const void *grad, int64_t grad_stride, const void *rows, int64_t rows_stride,
-                         const int32_t *row_of_slot, const int32_t *last_end, const float *weights, void *d_rows,
+                         const int32_t *row_of_slot, const int32_t *ends, int E, const float *weights, void *d_rows,
                          int64_t d_rows_stride, float *d_weights, int64_t tokens, int32_t choices, int64_t cols,
                          cudaStream_t stream) {
     using P = Raw<T, N>;
@@ -557,7 +556,7 @@ mx_status backward_typed(const void *grad, int64_t grad_stride, const void *rows
     const int64_t ctas = warp ? div_up(tokens, kRowThreads / 32) : tokens;
     return launch(warp ? combine_backward_kernel<T, N, 32, kAhead> : combine_backward_kernel<T, N, kRowThreads, kAhead>, ctas,
                   kRowThreads, 0, stream, static_cast<const P *>(grad), grad_stride / N, static_cast<const P *>(rows),
-                  rows_stride / N, row_of_slot, last_end, weights, static_cast<P *>(d_rows), d_rows_stride / N, d_weights, s);
+                  rows_stride / N, row_of_slot, ends, E, weights, static_cast<P *>(d_rows), d_rows_stride / N, d_weights, s);
 }
 
 }  // namespace
@@ -606,8 +605,7 @@ mx_status mx_dispatch_rows(const void *x, mx_dtype dtype, int64_t tokens, int64_
     if (bytes < 8 && cols * es / 2 > mx::kOpsMaxExtent) return MX_ERR_UNSUPPORTED;
     int sms = 0;
     if (mx_status st = mx_device_sms(&sms); st != MX_OK) return st;
-    const int32_t *last = group_ends + num_experts - 1;
-#define MX_DISPATCH(F, P) mx::F<P>(x, x_stride * es, row_of_slot, last, out, out_stride * es, tokens, choices, cols * es, stream)
+#define MX_DISPATCH(F, P) mx::F<P>(x, x_stride * es, row_of_slot, group_ends, num_experts, out, out_stride * es, tokens, choices, cols * es, stream)
     return bytes == 16  ? MX_DISPATCH(dispatch_typed, uint4)
            : bytes == 8 ? MX_DISPATCH(dispatch_typed, uint2)
            : bytes == 4 ? MX_DISPATCH(dispatch_elements, uint32_t)
@@ -660,12 +658,11 @@ mx_status mx_combine_rows_backward(const void *grad, mx_dtype dtype, int64_t tok
         return MX_ERR_MISALIGNED;
     int sms = 0;
     if (mx_status st = mx_device_sms(&sms); st != MX_OK) return st;
-    const int32_t *last = group_ends + num_experts - 1;
     const mx::Mat mats[] = {{grad, grad_stride}, {rows, rows_stride}, {d_rows, d_rows_stride}};
     const int bytes = mx::pack_bytes(es, cols, mats);
 #define MX_BACKWARD_K(T, N, K)                                                                                            \
-    mx::backward_typed<T, N, K>(grad, grad_stride, rows, rows_stride, row_of_slot, last, weights, d_rows, d_rows_stride, \
-                                d_weights, tokens, choices, cols, stream)
+    mx::backward_typed<T, N, K>(grad, grad_stride, rows, rows_stride, row_of_slot, group_ends, num_experts, weights,      \
+                                d_rows, d_rows_stride, d_weights, tokens, choices, cols, stream)
 #define MX_BACKWARD(T, N) (choices <= 2 ? MX_BACKWARD_K(T, N, 2) : choices <= 4 ? MX_BACKWARD_K(T, N, 4) : MX_BACKWARD_K(T, N, 8))
 #define MX_BACKWARD_16(T) (bytes == 16 ? MX_BACKWARD(T, 8) : bytes == 8 ? MX_BACKWARD(T, 4) : bytes == 4 ? MX_BACKWARD(T, 2) : MX_BACKWARD(T, 1))
     if (dtype == MX_F32) return bytes == 16 ? MX_BACKWARD(float, 4) : bytes == 8 ? MX_BACKWARD(float, 2) : MX_BACKWARD(float, 1);

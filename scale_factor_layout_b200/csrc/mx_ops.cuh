@@ -44,6 +44,15 @@ mx_status launch(void (*kernel)(KArgs...), int64_t grid, int block, int smem, cu
     return e == cudaSuccess ? MX_OK : mx_record_cuda_error(e);
 }
 
+// Rows in groups, which is the first row behind the last group: the largest of the
+// ends, as the group table's clamping has it (the table's cap, the number of rows,
+// is left to the caller).  For whole warps.
+__device__ __forceinline__ int rows_in_groups(const int *ends, int G) {
+    const int lane = threadIdx.x & 31;
+    const int e0 = lane < G ? __ldg(ends + lane) : 0, e1 = lane + 32 < G ? __ldg(ends + lane + 32) : 0;
+    return max(0, __reduce_max_sync(0xffffffffu, max(e0, e1)));
+}
+
 template <typename T> __device__ __forceinline__ T from_f32(float v);
 template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }

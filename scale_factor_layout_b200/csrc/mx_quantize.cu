@@ -177,7 +177,8 @@ struct RowsArgs {
     uint8_t *scales;
     int64_t scale_row, scale_block;   // bytes between the scales of neighbouring rows and blocks
     const int *row_of_slot;           // kOrder: the rows that each token goes to
-    const int *last_end;
+    const int *ends;
+    int32_t G;
     int64_t in_rows, out_rows;
     int32_t cols, k, segments;
     int32_t per_warp;                 // rows of a warp, 1 to 4
@@ -250,8 +251,7 @@ quantize_rows_kernel(const T *__restrict__ x, int64_t x_stride, RowsArgs a) {
         }
     }
     if (kOrder) {   // rows behind the last group
-        int64_t from = *a.last_end;
-        if (from < 0) from = 0;
+        const int64_t from = rows_in_groups(a.ends, a.G);
         const int64_t units = (a.cols + 7) / 8, n = (a.out_rows - from) * units;
         for (int64_t i = (int64_t)blockIdx.x * kQThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kQThreads) {
             const int64_t r = from + i / units;
@@ -475,7 +475,8 @@ mx_status mx_quantize_rows(const void *x, mx_dtype dtype, int64_t rows, int64_t 
     a.scale_row = scale_row_stride;
     a.scale_block = scale_block_stride;
     a.row_of_slot = row_of_slot;
-    a.last_end = order ? group_ends + num_experts - 1 : nullptr;
+    a.ends = group_ends;
+    a.G = num_experts;
     a.in_rows = rows;
     a.out_rows = order ? rows * choices : rows;
     a.cols = (int32_t)cols;

@@ -43,3 +43,26 @@ def test_sorts_of_threads_on_one_stream(mxlib):
         t.join(120)
     assert not errors, errors
     assert mxs.mx_device_flags() == 0
+
+
+@pytest.mark.parametrize("ends", [[100, 500, 20], [-5, 30, 10], [2**31 - 1, 0, 3], [45, 20, -2**31], [-1, -7, -2**31]])
+@pytest.mark.parametrize("C", [24, 33])
+def test_bad_ends_of_an_order_are_clamped(mxlib, ends, C):
+    """Ends that go back, below zero or past the rows are read as everywhere: rows of a group that they
+    cover are not zeroed as rows behind the last group."""
+    T, k = 30, 2
+    good = ref.clamp_ends(ends, T * k)
+    row = torch.arange(T * k, dtype=torch.int32).view(T, k)
+    row[row >= good[-1]] = -1
+    row = row.cuda()
+    bad, order = (mxs.ExpertOrder(torch.tensor(e, dtype=torch.int32, device="cuda"), row, row.reshape(-1)) for e in (ends, good))
+    gen = torch.Generator(device="cuda").manual_seed(C)
+    x, rows = (torch.randn(n, C, device="cuda", generator=gen).bfloat16() for n in (T, T * k))
+    w = torch.rand(T, k, device="cuda", generator=gen)
+    assert torch.equal(mxs.dispatch_rows(x, bad), mxs.dispatch_rows(x, order))
+    for got, want in zip(mxs.combine_rows_backward(x, rows, bad, w), mxs.combine_rows_backward(x, rows, order, w)):
+        assert torch.equal(got, want)
+    for block in (32, 128):
+        (q, s), (q2, s2) = mxs.quantize_rows(x, block=block, order=bad), mxs.quantize_rows(x, block=block, order=order)
+        assert torch.equal(q.view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s, s2)
+    assert (mxs.dispatch_rows(x, bad).abs().sum(1) > 0).sum() == good[-1]
