@@ -20,9 +20,12 @@ and its backward pass:
     d_weight = grouped_matmul_k(*quantize_cols(d_rows, order.group_ends, dtype=torch.float8_e5m2),
                                 *quantize_cols(dispatch_rows(x, order), order.group_ends), order.group_ends)
 
-``dispatch_rows`` and ``combine_rows`` are differentiable.  All calls run on
-torch's current stream of the tensors' device, allocate their outputs with
-torch and may be captured in a CUDA graph (after one call on the device).
+``dispatch_rows`` and ``combine_rows`` are differentiable, backward and once;
+forward-mode derivatives raise.  The other calls take no part in
+differentiation: their results carry no gradient, whatever their inputs do.
+All calls run on torch's current stream of the tensors' device, allocate their
+outputs with torch and may be captured in a CUDA graph (after one call on the
+device).
 """
 from __future__ import annotations
 
@@ -30,6 +33,7 @@ import functools
 from typing import NamedTuple
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _binding as B
 
@@ -198,6 +202,15 @@ class _Combine(torch.autograd.Function):
         return d_rows, d_weights, None, None, None
 
 
+def _wants_derivative(t: torch.Tensor, u: torch.Tensor | None = None) -> bool:
+    """Whether a result has to go through an autograd function.  A tangent of forward
+    mode has to as well: the functions have no rule for it, so that it raises there."""
+    if torch.is_grad_enabled() and (t.requires_grad or (u is not None and u.requires_grad)):
+        return True
+    return forward_ad._current_level >= 0 and (forward_ad.unpack_dual(t).tangent is not None or (
+        u is not None and forward_ad.unpack_dual(u).tangent is not None))
+
+
 def dispatch_rows(x: torch.Tensor, order: ExpertOrder, out: torch.Tensor | None = None) -> torch.Tensor:
     """Token rows ``x`` [tokens, cols] in expert order: [tokens * choices, cols],
     zeros behind the last group.  Differentiable in x (without ``out``)."""
@@ -207,7 +220,7 @@ def dispatch_rows(x: torch.Tensor, order: ExpertOrder, out: torch.Tensor | None 
     T, k = order.row_of_slot.shape
     if x.shape[0] != T:
         raise ValueError(f"x has {x.shape[0]} rows, the order {T} tokens")
-    wants_grad = torch.is_grad_enabled() and x.requires_grad
+    wants_grad = _wants_derivative(x)
     if out is not None:
         if wants_grad:
             raise ValueError("out cannot be given where a gradient is wanted")
@@ -237,7 +250,7 @@ def combine_rows(rows: torch.Tensor, order: ExpertOrder, weights: torch.Tensor |
     _check_rows_of(order, rows)
     if weights is not None:
         _check_weights(order, weights)
-    wants_grad = torch.is_grad_enabled() and (rows.requires_grad or (weights is not None and weights.requires_grad))
+    wants_grad = _wants_derivative(rows, weights)
     if out is not None:
         if wants_grad:
             raise ValueError("out cannot be given where a gradient is wanted")
