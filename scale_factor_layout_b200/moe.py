@@ -120,6 +120,15 @@ def _check_out(out: torch.Tensor, shape, dtypes) -> None:
     if tuple(out.shape) != tuple(shape) or out.dtype not in dtypes or (shape[-1] > 1 and out.stride(-1) != 1):
         raise ValueError(f"out must be a {', '.join(str(d) for d in dtypes)} tensor of shape {tuple(shape)}, "
                          "dense along columns")
+    if out.requires_grad and torch.is_grad_enabled():
+        raise ValueError("out cannot be a tensor that needs a gradient")
+
+
+def _written(out: torch.Tensor) -> torch.Tensor:
+    """A caller's tensor after a kernel has been launched that writes it: autograd is told."""
+    if not out.is_inference():
+        torch.autograd.graph.increment_version(out)
+    return out
 
 
 @functools.lru_cache(maxsize=1024)
@@ -154,22 +163,19 @@ def expert_sort(expert_ids: torch.Tensor, num_experts: int) -> ExpertOrder:
 # ------------------------------------------------------------------ rows to experts and back
 def _dispatch(x, order, out=None):
     T, k = order.row_of_slot.shape
-    if out is None:
-        out = x.new_empty(T * k, x.shape[1])
+    y = x.new_empty(T * k, x.shape[1]) if out is None else out
     _call("mx_dispatch_rows", x.device, x.data_ptr(), FLOATS[x.dtype], T, x.shape[1], _row_stride(x),
-          order.row_of_slot.data_ptr(), k, order.group_ends.data_ptr(), order.group_ends.numel(), out.data_ptr(),
-          _row_stride(out))
-    return out
+          order.row_of_slot.data_ptr(), k, order.group_ends.data_ptr(), order.group_ends.numel(), y.data_ptr(),
+          _row_stride(y))
+    return y if out is None else _written(out)
 
 
 def _combine(rows, order, weights, out=None):
     T, k = order.row_of_slot.shape
-    if out is None:
-        out = rows.new_empty(T, rows.shape[1])
+    y = rows.new_empty(T, rows.shape[1]) if out is None else out
     _call("mx_combine_rows", rows.device, rows.data_ptr(), FLOATS[rows.dtype], T, rows.shape[1], _row_stride(rows),
-          order.row_of_slot.data_ptr(), k, 0 if weights is None else weights.data_ptr(), out.data_ptr(),
-          _row_stride(out))
-    return out
+          order.row_of_slot.data_ptr(), k, 0 if weights is None else weights.data_ptr(), y.data_ptr(), _row_stride(y))
+    return y if out is None else _written(out)
 
 
 class _Dispatch(torch.autograd.Function):
@@ -425,14 +431,15 @@ def grouped_matmul(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_s
             if not s.is_contiguous() or s.numel() < need:
                 raise ValueError(f"{name} must be a contiguous blocked buffer of at least {need} bytes")
     if out is None:
-        out = torch.empty_strided((rows, n), (n, 1), dtype=out_dtype, device=a.device)
+        y = torch.empty_strided((rows, n), (n, 1), dtype=out_dtype, device=a.device)
     else:
         _check_out(out, (rows, n), (out_dtype,))
+        y = out
     _call("mx_grouped_matmul_m", a.device, a.data_ptr(), EIGHT_BIT[a.dtype], _row_stride(a, 16), a_scales.data_ptr(),
           a_row, a_block, b.data_ptr(), EIGHT_BIT[b.dtype], B.B_LAYOUTS[b_layout], b.stride(0), _row_stride(b, 16),
-          b_scales.data_ptr(), b_group, b_n, b_k, block, rows, n, k, group_ends.data_ptr(), G, out.data_ptr(),
-          FLOATS[out_dtype], _row_stride(out))
-    return out
+          b_scales.data_ptr(), b_group, b_n, b_k, block, rows, n, k, group_ends.data_ptr(), G, y.data_ptr(),
+          FLOATS[out_dtype], _row_stride(y))
+    return y if out is None else _written(out)
 
 
 def grouped_matmul_k(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scales: torch.Tensor,
@@ -458,11 +465,12 @@ def grouped_matmul_k(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b
         if cols > 1 and s.stride(1) != 1:
             raise ValueError(f"{name} must be dense along columns (stride(1) == 1)")
     if out is None:
-        out = torch.empty_strided((G, m, n), (m * n, n, 1), dtype=out_dtype, device=a.device)
+        y = torch.empty_strided((G, m, n), (m * n, n, 1), dtype=out_dtype, device=a.device)
     else:
         _check_out(out, (G, m, n), (out_dtype,))
+        y = out
     _call("mx_grouped_matmul_k", a.device, a.data_ptr(), EIGHT_BIT[a.dtype], _row_stride(a, 16), a_scales.data_ptr(),
           _row_stride(a_scales), b.data_ptr(), EIGHT_BIT[b.dtype], _row_stride(b, 16), b_scales.data_ptr(),
-          _row_stride(b_scales), padded, m, n, group_ends.data_ptr(), G, out.data_ptr(), FLOATS[out_dtype],
-          out.stride(0), _row_stride(out))
-    return out
+          _row_stride(b_scales), padded, m, n, group_ends.data_ptr(), G, y.data_ptr(), FLOATS[out_dtype],
+          y.stride(0), _row_stride(y))
+    return y if out is None else _written(out)

@@ -67,3 +67,47 @@ def test_forward_mode_derivatives_are_refused(launches, no_grad):
             mxs.combine_rows(rows, order, dual(w), out=torch.empty(4, 16))
         # without a tangent the calls are what they are elsewhere
         assert mxs.dispatch_rows(x, order).shape == (8, 16) and mxs.combine_rows(rows, order, w).shape == (4, 16)
+
+
+def out_calls():
+    """(name, call(out), shape, dtype) of every call that takes an output."""
+    f8, u8 = torch.float8_e4m3fn, torch.uint8
+    order, ends = small_order(), torch.zeros(2, dtype=torch.int32)
+    a, b, at, bt = (torch.zeros(s, dtype=f8) for s in ((4, 32), (2, 16, 32), (256, 16), (256, 32)))
+    s = lambda *shape: torch.zeros(shape, dtype=u8)   # noqa: E731
+    return [
+        ("dispatch_rows", lambda out: mxs.dispatch_rows(torch.ones(4, 16), order, out=out), (8, 16)),
+        ("combine_rows", lambda out: mxs.combine_rows(torch.ones(8, 16), order, torch.ones(4, 2), out=out), (4, 16)),
+        ("grouped_matmul", lambda out: mxs.grouped_matmul(a, s(4, 1), b, s(2, 1, 1), ends, out_dtype=torch.float32, out=out), (4, 16)),
+        ("grouped_matmul_k", lambda out: mxs.grouped_matmul_k(at, s(2, 16), bt, s(2, 32), ends, out_dtype=torch.float32, out=out), (2, 16, 32)),
+    ]
+
+
+OUT_CALLS = ["dispatch_rows", "combine_rows", "grouped_matmul", "grouped_matmul_k"]
+
+
+@pytest.mark.parametrize("name", OUT_CALLS)
+def test_a_written_output_is_known_to_autograd(launches, name):
+    """Writing into `out` counts as the change in place that it is: what was saved for a backward
+    pass and is overwritten raises there, instead of giving gradients from the new values."""
+    call, shape = next(c[1:] for c in out_calls() if c[0] == name)
+    out = torch.ones(shape)
+    leaf = torch.ones(shape, requires_grad=True)
+    loss = (leaf * out).sum()
+    assert call(out) is out
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():   # tensors without such a count
+        assert call(torch.ones(shape)).shape == shape
+
+
+@pytest.mark.parametrize("name", OUT_CALLS)
+def test_an_output_that_needs_a_gradient_is_refused(launches, name):
+    """Its gradient would be that of the values before the call."""
+    call, shape = next(c[1:] for c in out_calls() if c[0] == name)
+    leaf = torch.ones(shape, requires_grad=True)
+    for out in (leaf, leaf * 2):
+        with pytest.raises(ValueError, match="gradient"):
+            call(out)
+    with torch.no_grad():   # a parameter filled outside of any graph
+        assert call(leaf) is leaf
