@@ -25,11 +25,12 @@ forward-mode derivatives raise.  The other calls take no part in
 differentiation: their results carry no gradient, whatever their inputs do.
 All calls run on torch's current stream of the tensors' device, allocate their
 outputs with torch and may be captured in a CUDA graph (after one call on the
-device).
+device).  An ``out`` that is given must not overlap an input.
 """
 from __future__ import annotations
 
 import functools
+import math
 from typing import NamedTuple
 
 import torch
@@ -122,6 +123,32 @@ def _check_out(out: torch.Tensor, shape, dtypes) -> None:
                          "dense along columns")
     if out.requires_grad and torch.is_grad_enabled():
         raise ValueError("out cannot be a tensor that needs a gradient")
+
+
+def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether two tensors may share a byte: their spans do, and they are not columns
+    of one matrix beside each other."""
+    if not a.numel() or not b.numel():
+        return False
+    es, fs = a.element_size(), b.element_size()
+    span_a = (sum((n - 1) * s for n, s in zip(a.shape, a.stride())) + 1) * es
+    span_b = (sum((n - 1) * s for n, s in zip(b.shape, b.stride())) + 1) * fs
+    p, q = a.data_ptr(), b.data_ptr()
+    if p + span_a <= q or q + span_b <= p:
+        return False
+    # rows start at multiples of `pitch` from the first one's start
+    pitch = math.gcd(*(s * es for n, s in zip(a.shape[:-1], a.stride()) if n > 1),
+                     *(s * fs for n, s in zip(b.shape[:-1], b.stride()) if n > 1))
+    if pitch == 0:
+        return True
+    at = (q - p) % pitch
+    return at < ((a.shape[-1] - 1) * a.stride(-1) + 1) * es or at + ((b.shape[-1] - 1) * b.stride(-1) + 1) * fs > pitch
+
+
+def _check_apart(out: torch.Tensor, **inputs) -> None:
+    for name, t in inputs.items():
+        if t is not None and _overlap(out, t):
+            raise ValueError(f"out overlaps {name}")
 
 
 def _written(out: torch.Tensor) -> torch.Tensor:
@@ -231,6 +258,7 @@ def dispatch_rows(x: torch.Tensor, order: ExpertOrder, out: torch.Tensor | None 
         if wants_grad:
             raise ValueError("out cannot be given where a gradient is wanted")
         _check_out(out, (T * k, x.shape[1]), (x.dtype,))
+        _check_apart(out, x=x, group_ends=order.group_ends, row_of_slot=order.row_of_slot)
     return _Dispatch.apply(x, *order) if wants_grad else _dispatch(x, order, out)
 
 
@@ -261,6 +289,7 @@ def combine_rows(rows: torch.Tensor, order: ExpertOrder, weights: torch.Tensor |
         if wants_grad:
             raise ValueError("out cannot be given where a gradient is wanted")
         _check_out(out, (order.row_of_slot.shape[0], rows.shape[1]), (rows.dtype,))
+        _check_apart(out, rows=rows, row_of_slot=order.row_of_slot, weights=weights)
     return _Combine.apply(rows, weights, *order) if wants_grad else _combine(rows, order, weights, out)
 
 
@@ -434,6 +463,7 @@ def grouped_matmul(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_s
         y = torch.empty_strided((rows, n), (n, 1), dtype=out_dtype, device=a.device)
     else:
         _check_out(out, (rows, n), (out_dtype,))
+        _check_apart(out, a=a, a_scales=a_scales, b=b, b_scales=b_scales, group_ends=group_ends)
         y = out
     _call("mx_grouped_matmul_m", a.device, a.data_ptr(), EIGHT_BIT[a.dtype], _row_stride(a, 16), a_scales.data_ptr(),
           a_row, a_block, b.data_ptr(), EIGHT_BIT[b.dtype], B.B_LAYOUTS[b_layout], b.stride(0), _row_stride(b, 16),
@@ -468,6 +498,7 @@ def grouped_matmul_k(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b
         y = torch.empty_strided((G, m, n), (m * n, n, 1), dtype=out_dtype, device=a.device)
     else:
         _check_out(out, (G, m, n), (out_dtype,))
+        _check_apart(out, a=a, a_scales=a_scales, b=b, b_scales=b_scales, group_ends=group_ends)
         y = out
     _call("mx_grouped_matmul_k", a.device, a.data_ptr(), EIGHT_BIT[a.dtype], _row_stride(a, 16), a_scales.data_ptr(),
           _row_stride(a_scales), b.data_ptr(), EIGHT_BIT[b.dtype], _row_stride(b, 16), b_scales.data_ptr(),

@@ -111,3 +111,50 @@ def test_an_output_that_needs_a_gradient_is_refused(launches, name):
             call(out)
     with torch.no_grad():   # a parameter filled outside of any graph
         assert call(leaf) is leaf
+
+
+def test_an_output_that_overlaps_an_input_is_refused(launches):
+    """Kernels read rows while others are written: the same memory cannot be both."""
+    order, f32 = small_order(), torch.float32
+    buf = torch.ones(16, 16)
+    with pytest.raises(ValueError, match="out overlaps x"):
+        mxs.dispatch_rows(buf[:4], order, out=buf[:8])
+    with pytest.raises(ValueError, match="out overlaps x"):
+        mxs.dispatch_rows(buf[7:11], order, out=buf[:8])
+    with pytest.raises(ValueError, match="out overlaps rows"):
+        mxs.combine_rows(buf[:8], order, out=buf[:4])
+    with pytest.raises(ValueError, match="out overlaps rows"):
+        mxs.combine_rows(buf[:8, :8], order, out=buf[4:8, 7:15])
+    w = torch.ones(8, 2)
+    with pytest.raises(ValueError, match="out overlaps weights"):
+        mxs.combine_rows(torch.ones(8, 2), order, w[:4], out=w[2:6])
+    memory = torch.zeros(1 << 14, dtype=torch.uint8)
+    f8, ends = torch.float8_e4m3fn, torch.zeros(2, dtype=torch.int32)
+    a, b, sa, sb = (torch.zeros(s, dtype=t) for s, t in (((4, 32), f8), ((2, 16, 32), f8), ((4, 1), torch.uint8), ((2, 1, 1), torch.uint8)))
+    place = lambda like, at: memory[at: at + like.numel()].view(like.dtype).view(like.shape)   # noqa: E731
+    out = memory[:4 * 16 * 4].view(f32).view(4, 16)
+    for i, name in enumerate(("a", "a_scales", "b", "b_scales")):
+        given = [a, sa, b, sb]
+        given[i] = place(given[i], 255)   # the last byte of out
+        with pytest.raises(ValueError, match=f"out overlaps {name}"):
+            mxs.grouped_matmul(*given, ends, out_dtype=f32, out=out)
+        given[i] = place(given[i], 256)
+        assert mxs.grouped_matmul(*given, ends, out_dtype=f32, out=out) is out
+    at, bt, s, t = (torch.zeros(s, dtype=d) for s, d in (((256, 16), f8), ((256, 32), f8), ((2, 16), torch.uint8), ((2, 32), torch.uint8)))
+    out = memory[:2 * 16 * 32 * 4].view(f32).view(2, 16, 32)
+    with pytest.raises(ValueError, match="out overlaps b"):
+        mxs.grouped_matmul_k(at, s, place(bt, 4000), t, ends, out_dtype=f32, out=out)
+
+
+def test_an_output_beside_its_input_is_taken(launches):
+    """Neighbours in one buffer do not overlap: rows behind rows, columns beside columns, every other row."""
+    order, buf = small_order(), torch.ones(16, 32)
+    assert mxs.dispatch_rows(buf[8:12], order, out=buf[:8]).shape == (8, 32)
+    assert mxs.dispatch_rows(buf[:4, :16], order, out=buf[:8, 16:]).shape == (8, 16)
+    assert mxs.combine_rows(buf[0::2], order, out=buf[1::2][:4]).shape == (4, 32)
+    assert mxs.combine_rows(buf[:8, 20:30], order, out=buf[2:6, 10:20]).shape == (4, 10)
+    assert mxs.combine_rows(buf[:8, :0], order, out=buf[:4, :0]).shape == (4, 0)
+    one = small_order(tokens=1, choices=1)
+    assert mxs.combine_rows(buf[:1, :8], one, out=buf[:1, 8:16]).shape == (1, 8)
+    with pytest.raises(ValueError, match="overlaps"):
+        mxs.combine_rows(buf[:1, :8], one, out=buf[:1, 7:15])
