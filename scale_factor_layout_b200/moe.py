@@ -40,6 +40,7 @@ from . import _binding as B
 
 FLOATS = {torch.float32: B.MX_F32, torch.bfloat16: B.MX_BF16, torch.float16: B.MX_F16}
 EIGHT_BIT = {torch.float8_e4m3fn: B.MX_E4M3, torch.float8_e5m2: B.MX_E5M2}
+MAX_SLOTS = 2**31 - 2**14   # the library's largest extent; choices go into it as 32-bit numbers
 
 
 class ExpertOrder(NamedTuple):
@@ -115,6 +116,8 @@ def _check_order(order: ExpertOrder) -> None:
     r = order.row_of_slot
     if r.dtype != torch.int32 or r.dim() != 2 or not r.is_contiguous() or r.shape[1] < 1:
         raise ValueError("order.row_of_slot must be a contiguous int32 tensor [tokens, choices]")
+    if r.numel() > MAX_SLOTS:
+        raise ValueError(f"order.row_of_slot must hold at most {MAX_SLOTS} slots")
 
 
 def _check_out(out: torch.Tensor, shape, dtypes) -> None:
@@ -175,6 +178,8 @@ def expert_sort(expert_ids: torch.Tensor, num_experts: int) -> ExpertOrder:
     if k < 1:
         raise ValueError("expert_ids must have at least one choice a token")
     dev, i32, S = expert_ids.device, torch.int32, T * k
+    if S > MAX_SLOTS:
+        raise ValueError(f"expert_ids must hold at most {MAX_SLOTS} slots")
     ends = torch.empty_strided((num_experts,), (1,), dtype=i32, device=dev)
     row_of_slot = torch.empty_strided((T, k), (k, 1), dtype=i32, device=dev)
     slot_of_row = torch.empty_strided((S,), (1,), dtype=i32, device=dev)

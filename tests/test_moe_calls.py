@@ -158,3 +158,21 @@ def test_an_output_beside_its_input_is_taken(launches):
     assert mxs.combine_rows(buf[:1, :8], one, out=buf[:1, 8:16]).shape == (1, 8)
     with pytest.raises(ValueError, match="overlaps"):
         mxs.combine_rows(buf[:1, :8], one, out=buf[:1, 7:15])
+
+
+@pytest.mark.parametrize("choices", [2**31 - 2**14 + 1, 2**32 + 2])
+def test_more_slots_than_31_bits_are_refused(mxlib, launches, choices):
+    """Their number would lose its upper bits on the way into the library."""
+    ids = torch.empty(1, choices, dtype=torch.int32, device="meta")
+    with pytest.raises(ValueError, match="slots"):
+        mxs.expert_sort(ids, 4)
+    order = small_order()._replace(row_of_slot=ids)
+    x = torch.empty(1, 16, device="meta")
+    for call in (lambda: mxs.dispatch_rows(x, order), lambda: mxs.quantize_rows(x, order=order),
+                 lambda: mxs.combine_rows(torch.empty(choices, 16, device="meta"), order),
+                 lambda: mxs.combine_rows_backward(x, torch.empty(choices, 16, device="meta"), order, torch.empty(1, choices, device="meta"))):
+        with pytest.raises(ValueError, match="slots"):
+            call()
+    assert not launches
+    most = torch.empty(1, 2**31 - 2**14, dtype=torch.int32, device="meta")
+    assert mxs.expert_sort(most, 4).row_of_slot.shape == most.shape
