@@ -10,6 +10,8 @@ torch's current CUDA stream.
 """
 from __future__ import annotations
 
+from importlib import util as _util
+
 from ._binding import (  # noqa: F401
     MX_GROUPS_K, MX_GROUPS_M, MX_MAX_GROUPS, MX_OK, MX_PATH_AUTO, MX_PATH_BYTE, MX_PATH_FLAT, MX_PATH_TMA,
     MX_PATH_WORD, PATHS, MxError, declared_symbols, lib, mx_device_flags, mx_rearrange_ex,
@@ -23,8 +25,18 @@ _MOE = (
     "quantize_cols", "quantize_blocks", "grouped_matmul", "grouped_matmul_k",
 )
 
+
+
+def _has_torch() -> bool:
+    try:
+        return _util.find_spec("torch") is not None
+    except (ImportError, ValueError):
+        return False
+
+
+# all names are to be had without torch as well: the operators are among them where it is installed
 __all__ = [
-    *_MOE,
+    *(_MOE if _has_torch() else ()),
     "rearrange_m_groups", "rearrange_k_groups", "rearrange", "rearranged_size",
     "mx_rearrange_m_groups", "mx_rearrange_k_groups", "mx_rearrange_ex", "mx_rearranged_size",
     "mx_select_path", "mx_device_flags", "mx_version", "MxError", "unrearrange", "padded_group_starts",
