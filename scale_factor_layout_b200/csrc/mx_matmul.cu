@@ -83,7 +83,7 @@ struct MatArgs {
     int32_t n_tiles, m_tiles, k_tiles;      // m_tiles: contraction groups only
     int32_t out_type;                       // 0 f32, 1 bf16, 2 f16
     uint32_t idesc;
-    bool tma_out;                           // out's rows start on 16-byte boundaries
+    bool tma_out;                           // out's rows start and end on 16-byte boundaries
     bool swapped;                           // contraction groups: tiles are of out's transpose
 };
 
@@ -397,7 +397,7 @@ __device__ __forceinline__ void add_parts(uint8_t *stages, const Tile &o, const 
             sum[4] += y.x, sum[5] += y.y, sum[6] += y.z, sum[7] += y.w;
         }
         const int64_t at = (kForm == kFormOuter ? o.g * a.out_group : 0) + (int64_t)(o.row0 + r) * a.out_stride + n;
-        if (a.tma_out && es == 2 && n + 8 <= a.N) {
+        if (a.tma_out && es == 2) {   // N is then a multiple of 8
             *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at) =
                 a.out_type == 1 ? pack<__nv_bfloat16, 8>(sum) : pack<__half, 8>(sum);
         } else {
@@ -807,6 +807,14 @@ mx_status tiles_map(CUtensorMap *map, const void *p, int64_t tiles) {
     return mx_encode_map(map, p, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+// Whether the output may be stored as boxes of a tensor map.  A row has to end on a
+// 16-byte boundary too: a store of bytes is cut at the row's end rounded up to 16 (what
+// lay behind 2441 columns of bf16 was overwritten up to the 2448th), so that it would
+// reach into whatever lies between the rows.
+bool boxes_out(const void *p, int64_t n, int64_t es, int64_t stride, int64_t group_stride) {
+    return aligned_to(p, 16) && n * es % 16 == 0 && stride * es % 16 == 0 && group_stride * es % 16 == 0;
+}
+
 // The output in bytes, 32 rows x 64 bytes a box.
 mx_status out_map(CUtensorMap *map, const void *p, int64_t row_bytes, int64_t rows, int64_t stride, int64_t groups, int64_t group_stride) {
     const uint64_t dims[3] = {(uint64_t)row_bytes, (uint64_t)rows, (uint64_t)groups};
@@ -918,7 +926,7 @@ mx_status mx_grouped_matmul_m(const void *a, mx_dtype a_dtype, int64_t a_stride,
     m.N = (int32_t)n;
     m.k_tiles = (int32_t)div_up(k, kTileK);
     m.out_type = out_code(out_dtype);
-    m.tma_out = aligned_to(out, 16) && (out_stride * os) % 16 == 0;
+    m.tma_out = boxes_out(out, n, os, out_stride, 0);
     m.idesc = block_scaled_idesc(a_dtype == MX_E5M2, b_dtype == MX_E5M2, false, !nk);
     int sms = 0;
     if (mx_status st = mx_device_sms(&sms); st != MX_OK) return st;
@@ -988,7 +996,7 @@ mx_status mx_grouped_matmul_k(const void *a, mx_dtype a_dtype, int64_t a_stride,
     g.M = (int32_t)m;
     g.N = (int32_t)n;
     g.out_type = out_code(out_dtype);
-    g.tma_out = aligned_to(out, 16) && (out_stride * os) % 16 == 0 && (g.out_group * os) % 16 == 0;
+    g.tma_out = boxes_out(out, n, os, out_stride, g.out_group);
     g.idesc = block_scaled_idesc(a_dtype == MX_E5M2, b_dtype == MX_E5M2, true, true);
     Maps maps = {};
     if (mx_status st = operand_map(&maps.a, a, m, padded_rows, a_stride, 0, 0, 128); st != MX_OK) return st;

@@ -66,3 +66,35 @@ def test_bad_ends_of_an_order_are_clamped(mxlib, ends, C):
         (q, s), (q2, s2) = mxs.quantize_rows(x, block=block, order=bad), mxs.quantize_rows(x, block=block, order=order)
         assert torch.equal(q.view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s, s2)
     assert (mxs.dispatch_rows(x, bad).abs().sum(1) > 0).sum() == good[-1]
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("sizes,behind,N,K", [
+    ([200], 40, 131, 256),            # 128 x 128 tiles
+    ([100] * 12, 0, 2441, 128),       # 128 x 256 tiles
+    ([600, 0, 1000], 70, 2437, 256),  # pairs of CTAs
+    ([40], 0, 129, 2304),             # a contraction that CTAs share
+])
+def test_products_write_nothing_beside_their_rows(mxlib, sizes, behind, N, K, out):
+    """Rows that start on 16-byte boundaries and end off them, in the middle of a larger matrix."""
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    R, G = sum(sizes) + behind, len(sizes)
+    ends = torch.tensor(np.cumsum(sizes), dtype=torch.int32, device="cuda")
+    (a, sa), (b, sb) = mxs.quantize_rows(torch.randn(R, K, device="cuda", generator=gen)), mxs.quantize_blocks(torch.randn(G, N, K, device="cuda", generator=gen))
+    P = ref.up(R, 128) + 128 * G
+    at, sat = mxs.quantize_cols(torch.randn(R, 300, device="cuda", generator=gen), ends)
+    bt, sbt = mxs.quantize_cols(torch.randn(R, N, device="cuda", generator=gen), ends)
+    assert at.shape[0] == P
+
+    def check(call, shape):
+        want = call(None)
+        stride = ref.up(N, 8) + 8
+        buf = torch.full((int(np.prod(shape[:-1])) + 2, stride), 77.0, dtype=out, device="cuda")
+        inner = buf[1:-1].view(*shape[:-1], stride)[..., :N]
+        assert inner.data_ptr() % 16 == 0 and torch.equal(call(inner), want)
+        assert buf[:, N:].eq(77).all() and buf[0].eq(77).all() and buf[-1].eq(77).all()
+
+    check(lambda o: mxs.grouped_matmul(a, sa, b, sb, ends, out_dtype=out, out=o), (R, N))
+    check(lambda o: mxs.grouped_matmul_k(at, sat, bt, sbt, ends, out_dtype=out, out=o), (G, 300, N))
+    check(lambda o: mxs.grouped_matmul_k(bt, sbt, bt, sbt, ends, out_dtype=out, out=o), (G, N, N))
+    assert mxs.mx_device_flags() == 0
