@@ -316,6 +316,17 @@ mx_status mx_grouped_matmul_k(const void *a, mx_dtype a_dtype, int64_t a_stride,
                               const int32_t *group_ends, int32_t num_groups, void *out, mx_dtype out_dtype,
                               int64_t out_group_stride, int64_t out_stride, cudaStream_t stream);
 
+/* How a grouped product is spread over the SMs: 128 x 128 tiles of one CTA each, or of
+ * 2, 4 or 8 CTAs that share a tile's contraction; 128 x 256 tiles; 256 x 256 tiles of
+ * pairs of CTAs, or of the transposed product (weight gradients only). */
+typedef enum { MX_TILES_NONE = 0, MX_TILES_NARROW = 1, MX_TILES_SPLIT_2 = 2, MX_TILES_SPLIT_4 = 4, MX_TILES_SPLIT_8 = 8,
+               MX_TILES_WIDE = 16, MX_TILES_PAIRS = 32, MX_TILES_PAIRS_ACROSS = 33 } mx_tiles;
+
+/* The tiles that the grouped products take on a device of `sms` SMs (host-only):
+ * MX_GROUPS_M for mx_grouped_matmul_m (m its rows), MX_GROUPS_K for
+ * mx_grouped_matmul_k (k its padded rows).  MX_TILES_NONE for invalid arguments. */
+mx_tiles mx_select_tiles(mx_group_dim dim, int64_t m, int64_t n, int64_t k, int32_t num_groups, int32_t sms);
+
 #ifdef __cplusplus
 }
 #endif

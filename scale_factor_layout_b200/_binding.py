@@ -24,6 +24,8 @@ PATHS = {"auto": MX_PATH_AUTO, "tma": MX_PATH_TMA, "word": MX_PATH_WORD, "byte":
 PATH_NAMES = {v: k for k, v in PATHS.items()}
 
 MX_F32, MX_BF16, MX_F16, MX_E4M3, MX_E5M2 = range(5)
+MX_TILES_NONE, MX_TILES_NARROW, MX_TILES_SPLIT_2, MX_TILES_SPLIT_4, MX_TILES_SPLIT_8 = 0, 1, 2, 4, 8
+MX_TILES_WIDE, MX_TILES_PAIRS, MX_TILES_PAIRS_ACROSS = 16, 32, 33
 MX_B_NK, MX_B_KN = 0, 1
 B_LAYOUTS = {"nk": MX_B_NK, "kn": MX_B_KN}
 
@@ -62,6 +64,7 @@ _SIGNATURES = {
                                            ctypes.c_int, _I64, _P]),
     "mx_grouped_matmul_k": (ctypes.c_int, [_P, ctypes.c_int, _I64, _P, _I64, _P, ctypes.c_int, _I64, _P, _I64, _I64,
                                            _I64, _I64, _P, _I32, _P, ctypes.c_int, _I64, _I64, _P]),
+    "mx_select_tiles": (ctypes.c_int, [ctypes.c_int, _I64, _I64, _I64, _I32, _I32]),
     "mx_last_cuda_error": (ctypes.c_int, []),
     "mx_version": (ctypes.c_int, []),
 }
@@ -235,3 +238,7 @@ def mx_grouped_matmul_k(a: int, a_dtype: int, a_stride: int, a_scales: int, a_sc
     return lib().mx_grouped_matmul_k(a, a_dtype, a_stride, a_scales, a_scale_stride, b, b_dtype, b_stride, b_scales,
                                      b_scale_stride, padded_rows, m, n, group_ends, num_groups, out, out_dtype,
                                      out_group_stride, out_stride, stream)
+
+
+def mx_select_tiles(dim: int, m: int, n: int, k: int, num_groups: int, sms: int) -> int:
+    return int(lib().mx_select_tiles(dim, m, n, k, num_groups, sms))

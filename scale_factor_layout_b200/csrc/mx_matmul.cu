@@ -856,6 +856,20 @@ Plan plan_of(int64_t row_tiles, int64_t most, int64_t n, int64_t rows, int64_t s
     // 256: 50 and 44, 512: 75 and 75; 8192 rows of one 8192 x 8192: 420 and 385.
     return {rows > 128 ? kPairs : kAlone, false, 1};
 }
+Plan plan_of_rows(int64_t rows, int64_t n, int64_t k, int64_t groups, int sms) {
+    const int64_t each = div_up(rows, groups), even = div_up(each, 128) * groups;
+    return plan_of(even < rows ? even : rows, most_row_tiles(rows, groups, 128), n, each, div_up(k, kTileK), sms);
+}
+Plan plan_of_contraction(int64_t m, int64_t n, int64_t padded_rows, int64_t groups, int sms) {
+    const int64_t row_tiles = div_up(m, 128) * groups;
+    return plan_of(row_tiles, row_tiles, n, m, padded_rows / kTileK / groups, sms);
+}
+// Pairs round their rows up to 256 and their columns to 32: where that makes the
+// transpose of a weight gradient cheaper, its tiles are computed and written across.
+// 1408 x 7168 in 8 groups of 131072 rows, bf16 out: 1040 us as it is, 980 us across.
+bool across(const Plan &plan, int64_t m, int64_t n) {
+    return plan.work == kPairs && 1.03 * up_to(n, 256) * up_to(m, 32) < (double)up_to(m, 256) * up_to(n, 32);
+}
 
 template <int kForm, int kScales>
 mx_status launch_planned(const Plan &p, const Maps &maps, const MatArgs &a, cudaStream_t stream) {
@@ -930,8 +944,7 @@ mx_status mx_grouped_matmul_m(const void *a, mx_dtype a_dtype, int64_t a_stride,
     m.idesc = block_scaled_idesc(a_dtype == MX_E5M2, b_dtype == MX_E5M2, false, !nk);
     int sms = 0;
     if (mx_status st = mx_device_sms(&sms); st != MX_OK) return st;
-    const int64_t each = div_up(rows, num_groups), even = div_up(each, 128) * num_groups;
-    const Plan plan = plan_of(even < rows ? even : rows, most_row_tiles(rows, num_groups, 128), n, each, m.k_tiles, sms);
+    const Plan plan = plan_of_rows(rows, n, k, num_groups, sms);
     const bool pair = plan.work == kPairs;
     Maps maps = {};
     if (mx_status st = operand_map(&maps.a, a, k, rows, a_stride, 0, 0, 128); st != MX_OK) return st;
@@ -978,8 +991,7 @@ mx_status mx_grouped_matmul_k(const void *a, mx_dtype a_dtype, int64_t a_stride,
 
     int sms = 0;
     if (mx_status st = mx_device_sms(&sms); st != MX_OK) return st;
-    const int64_t row_tiles = div_up(m, 128) * num_groups;
-    const Plan plan = plan_of(row_tiles, row_tiles, n, m, padded_rows / 128 / num_groups, sms);
+    const Plan plan = plan_of_contraction(m, n, padded_rows, num_groups, sms);
     MatArgs g = {};
     g.ends = group_ends;
     g.sa = a_scales;
@@ -1006,10 +1018,7 @@ mx_status mx_grouped_matmul_k(const void *a, mx_dtype a_dtype, int64_t a_stride,
                                    (num_groups > 1 ? out_group_stride : out_stride) * os);
             st != MX_OK)
             return st;
-    // Pairs round their rows up to 256 and their columns to 32: where that makes the
-    // transpose cheaper, its tiles are computed and written across.  1408 x 7168 in 8
-    // groups of 131072 rows, bf16 out: 1040 us as it is, 980 us across.
-    if (plan.work == kPairs && 1.03 * up_to(n, 256) * up_to(m, 32) < (double)up_to(m, 256) * up_to(n, 32)) {
+    if (across(plan, m, n)) {
         const CUtensorMap t = maps.a;
         maps.a = maps.b;
         maps.b = t;
@@ -1023,6 +1032,17 @@ mx_status mx_grouped_matmul_k(const void *a, mx_dtype a_dtype, int64_t a_stride,
         g.swapped = true;
     }
     return launch_planned<kFormOuter, kScales128>(plan, maps, g, stream);
+}
+
+mx_tiles mx_select_tiles(mx_group_dim dim, int64_t m, int64_t n, int64_t k, int32_t num_groups, int32_t sms) {
+    using namespace mx;
+    if ((dim != MX_GROUPS_M && dim != MX_GROUPS_K) || m < 1 || n < 1 || k < 1 || sms < 1 || num_groups < 1 ||
+        num_groups > MX_MAX_GROUPS || m > kOpsMaxExtent || n > kOpsMaxExtent || k > kOpsMaxExtent)
+        return MX_TILES_NONE;
+    const bool rows = dim == MX_GROUPS_M;
+    const Plan plan = rows ? plan_of_rows(m, n, k, num_groups, sms) : plan_of_contraction(m, n, k, num_groups, sms);
+    if (plan.work == kPairs) return !rows && across(plan, m, n) ? MX_TILES_PAIRS_ACROSS : MX_TILES_PAIRS;
+    return plan.work == kSplits ? (mx_tiles)plan.parts : plan.narrow ? MX_TILES_NARROW : MX_TILES_WIDE;
 }
 
 }  // extern "C"
