@@ -98,3 +98,40 @@ def test_products_write_nothing_beside_their_rows(mxlib, sizes, behind, N, K, ou
     check(lambda o: mxs.grouped_matmul_k(at, sat, bt, sbt, ends, out_dtype=out, out=o), (G, 300, N))
     check(lambda o: mxs.grouped_matmul_k(bt, sbt, bt, sbt, ends, out_dtype=out, out=o), (G, N, N))
     assert mxs.mx_device_flags() == 0
+
+
+def test_a_captured_training_step(mxlib):
+    """Dispatch and combine with their autograd backward in one graph, replayed on new inputs; a sort of
+    more slots than one CTA takes, so that its workspace is the graph's."""
+    T, k, E, C = 1100, 3, 5, 72
+    gen = torch.Generator(device="cuda").manual_seed(0)
+
+    def fresh():
+        return (torch.randn(T, C, device="cuda", generator=gen), torch.rand(T, k, device="cuda", generator=gen),
+                torch.randint(-1, E, (T, k), device="cuda", generator=gen))
+
+    def step(x, w, ids):
+        order = mxs.expert_sort(ids, E)
+        y = mxs.combine_rows(mxs.dispatch_rows(x, order).square(), order, w)
+        return (y, *torch.autograd.grad(y.sin().sum(), (x, w)))
+
+    x, w, ids = fresh()
+    x.requires_grad_()
+    w.requires_grad_()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(x, w, ids)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(x, w, ids)
+    for _ in range(3):
+        new = fresh()
+        with torch.no_grad():
+            for dst, src in zip((x, w, ids), new):
+                dst.copy_(src)
+        graph.replay()
+        want = step(new[0].requires_grad_(), new[1].requires_grad_(), new[2])
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
