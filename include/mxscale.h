@@ -205,9 +205,11 @@ int mx_version(void);
  * skipped, never followed.
  *
  * Strides are in elements, and below 2^40 bytes (MX_ERR_UNSUPPORTED).  Outputs must not overlap inputs.  Streams, graphs,
- * contexts and the bounded waits are as described above.  Any alignment and
- * stride is taken; rows that start on 16-byte boundaries are moved 16 bytes at
- * a time, others 8, 4 or one element's.  The product alone asks for 16-byte
+ * contexts and the bounded waits are as described above.  Pointers
+ * are aligned to their elements (MX_ERR_MISALIGNED) and rows are at least their
+ * length apart (MX_ERR_INVALID_ARG); beyond that any alignment and stride is taken.
+ * Rows that start on 16-byte boundaries are moved 16 bytes at a time, others less,
+ * and nothing is written beside the rows of an output.  The product alone asks for 16-byte
  * aligned operand rows; its contraction is at most 2^25 long, and a row of its
  * output 2^31 - 1 bytes (MX_ERR_UNSUPPORTED). */
 typedef enum { MX_F32 = 0, MX_BF16 = 1, MX_F16 = 2, MX_E4M3 = 3, MX_E5M2 = 4 } mx_dtype;

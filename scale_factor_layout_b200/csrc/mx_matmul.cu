@@ -36,12 +36,14 @@
 // 530 clocks, 512 of them the matrix instructions'), and 446 us (2.46 PFLOP/s)
 // after seconds of it, when the power limit holds the SMs near 1.3 GHz; a
 // library product of the same operands without scales per block takes 357 and
-// 418.  131072 x 1408 x 7168 in 8 ragged groups: 960 us, 2.75 PFLOP/s.  Few rows
-// are bound by the weights' bytes: 128 rows over 64 experts of 1408 x 7168, about
-// 50 of them in use, 88 us, 5.7 TB/s.
+// 418.  131072 x 1408 x 7168 in 8 ragged groups: 1140 to 1180 us of it (2.25 to 2.33
+// PFLOP/s), 960 us on a cool GPU.  Few rows are bound by the weights' bytes: 128 rows
+// over 64 experts of 1408 x 7168, about 50 of them in use, 88 to 106 us by the GPU, 4.8
+// to 5.7 TB/s.
 //
 // The sums are those of the tensor cores: 32 bits, but cut rather than rounded
-// at each step of 32; sums of 8192 positive products are off by 3.7e-6.
+// at each step of 32, and in one accumulator however long they are; sums of 8192
+// positive products are off by 3.7e-6, of 131072 by 1.5e-4 at most.
 
 #include <climits>
 #include <mutex>
@@ -866,7 +868,9 @@ Plan plan_of_contraction(int64_t m, int64_t n, int64_t padded_rows, int64_t grou
 }
 // Pairs round their rows up to 256 and their columns to 32: where that makes the
 // transpose of a weight gradient cheaper, its tiles are computed and written across.
-// 1408 x 7168 in 8 groups of 131072 rows, bf16 out: 1040 us as it is, 980 us across.
+// bf16 out, as it is and across: 1408 x 7168 in 8 groups of 131072 rows 958 and 926
+// us, 1152 x 8192 in 4 of 65536 533 and 498, 1408 x 2560 in 4 of 16384 86 and 85, but
+// 1300 x 5120 in 8 of 131072 772 and 778, 1408 x 4096 in 16 of 65536 347 and 367.
 bool across(const Plan &plan, int64_t m, int64_t n) {
     return plan.work == kPairs && 1.03 * up_to(n, 256) * up_to(m, 32) < (double)up_to(m, 256) * up_to(n, 32);
 }

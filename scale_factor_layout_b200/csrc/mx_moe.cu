@@ -169,7 +169,7 @@ sort_place_kernel(const Id *__restrict__ ids, int64_t S, int64_t per_cta, int64_
 // packs a thread, tpr packs apart (tpr a power of two: the packs of a row, at
 // most 256).  Chunks of a token are neighbours in the grid, so their rows are
 // touched together.  A pack is 16 bytes, 8, 4, or one element, whichever all rows
-// are aligned to.
+// are aligned to; the copy of rows off 8-byte boundaries has a kernel of its own.
 constexpr int kRowThreads = 256;
 
 struct RowShape {
@@ -207,9 +207,11 @@ __device__ __forceinline__ void place_of(const RowShape &s, int64_t &t, int &p) 
 // Rows off 8-byte boundaries, as elements of 16 bits (32-bit ones are two).  Loads
 // are of whole words (one that holds a wanted element is always readable), shifted
 // by an element where the row starts between two; stores are of 16 bytes from the
-// row's first boundary on, so that no sector is written in parts but at a row's
-// ends.  48033 tokens x 4 x 2201 bf16: 235 us, element by element 393; 2202, 4-byte
-// boundaries: 228, in packs of 4 bytes 260; 29144 x 1 x 2463: 87 and 145.
+// row's first boundary on, so that no sector of a token's row is written in parts but
+// at its ends.  48033 tokens x 4 x 2201 bf16: 235 us, element by element 393; 2202,
+// 4-byte boundaries: 228, in packs of 4 bytes 260; 29144 x 1 x 2463: 87 and 145.  Rows
+// behind the last group are still zeroed 4 or 2 bytes at a time: with half of those
+// slots dropped the first takes 494 us, with seven of eight 725.
 
 // Elements at .. at + 15 of a row; those past its `cols` are undefined.
 __device__ __forceinline__ void load_sixteen(const uint16_t *row, int at, int cols, uint32_t (&w)[8]) {
@@ -224,7 +226,6 @@ __device__ __forceinline__ void load_sixteen(const uint16_t *row, int at, int co
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i] = at - odd + 2 * i < cols ? __ldg(src + i) : 0u;
-        if (odd && at + 15 < cols) last = __ldg(src + 8);
     }
     if (odd) {
 #pragma unroll

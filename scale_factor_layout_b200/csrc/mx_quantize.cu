@@ -13,7 +13,7 @@
 // Everything here is bound by memory.  A thread holds 8 or 16 consecutive
 // elements, because a block of 128 is then 16 or 8 neighbouring lanes and its
 // maximum 4 or 3 shuffles.  On a B200, 131072 x 7168 bf16: rows 411 us (6.85
-// TB/s; 8 elements a lane 522), columns of 8 groups 470 us (6.0 TB/s), 128 x 128
+// TB/s; 8 elements a lane 522; blocks of 32 439), columns of 8 groups 470 us (6.0 TB/s), 128 x 128
 // blocks 455 us (6.2 TB/s); 16384 tokens to 131072 rows in expert order 217 us
 // (5.4 TB/s), 23 of them for the scales, whose bytes go to scattered rows.
 
