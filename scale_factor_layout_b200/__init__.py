@@ -26,7 +26,6 @@ _MOE = (
 )
 
 
-
 def _has_torch() -> bool:
     try:
         return _util.find_spec("torch") is not None

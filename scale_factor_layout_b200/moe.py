@@ -120,11 +120,20 @@ def _check_order(order: ExpertOrder) -> None:
         raise ValueError(f"order.row_of_slot must hold at most {MAX_SLOTS} slots")
 
 
+def _wants_derivative(t: torch.Tensor, u: torch.Tensor | None = None) -> bool:
+    """Whether a result has to go through an autograd function.  A tangent of forward
+    mode has to as well: the functions have no rule for it, so that it raises there."""
+    if torch.is_grad_enabled() and (t.requires_grad or (u is not None and u.requires_grad)):
+        return True
+    return forward_ad._current_level >= 0 and (forward_ad.unpack_dual(t).tangent is not None or (
+        u is not None and forward_ad.unpack_dual(u).tangent is not None))
+
+
 def _check_out(out: torch.Tensor, shape, dtypes) -> None:
     if tuple(out.shape) != tuple(shape) or out.dtype not in dtypes or (shape[-1] > 1 and out.stride(-1) != 1):
         raise ValueError(f"out must be a {', '.join(str(d) for d in dtypes)} tensor of shape {tuple(shape)}, "
                          "dense along columns")
-    if out.requires_grad and torch.is_grad_enabled():
+    if _wants_derivative(out):
         raise ValueError("out cannot be a tensor that needs a gradient")
 
 
@@ -238,15 +247,6 @@ class _Combine(torch.autograd.Function):
             return _dispatch(grad, order), None, None, None, None
         d_rows, d_weights = combine_rows_backward(grad, ctx.saved_tensors[3], order, ctx.saved_tensors[4])
         return d_rows, d_weights, None, None, None
-
-
-def _wants_derivative(t: torch.Tensor, u: torch.Tensor | None = None) -> bool:
-    """Whether a result has to go through an autograd function.  A tangent of forward
-    mode has to as well: the functions have no rule for it, so that it raises there."""
-    if torch.is_grad_enabled() and (t.requires_grad or (u is not None and u.requires_grad)):
-        return True
-    return forward_ad._current_level >= 0 and (forward_ad.unpack_dual(t).tangent is not None or (
-        u is not None and forward_ad.unpack_dual(u).tangent is not None))
 
 
 def dispatch_rows(x: torch.Tensor, order: ExpertOrder, out: torch.Tensor | None = None) -> torch.Tensor:

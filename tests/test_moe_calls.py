@@ -176,3 +176,20 @@ def test_more_slots_than_31_bits_are_refused(mxlib, launches, choices):
     assert not launches
     most = torch.empty(1, 2**31 - 2**14, dtype=torch.int32, device="meta")
     assert mxs.expert_sort(most, 4).row_of_slot.shape == most.shape
+
+
+@pytest.mark.parametrize("name", OUT_CALLS)
+def test_an_output_that_carries_a_tangent_is_refused(launches, name):
+    """Its tangent would be that of the values before the call."""
+    from torch.autograd import forward_ad
+
+    call, shape = next(c[1:] for c in out_calls() if c[0] == name)
+    with forward_ad.dual_level():
+        with pytest.raises(ValueError, match="gradient"):
+            call(forward_ad.make_dual(torch.ones(shape), torch.ones(shape)))
+        plain = torch.ones(shape)
+        assert call(plain) is plain
+    outside = torch.ones(shape)
+    with torch.inference_mode():   # a tensor that was made outside of it
+        before = outside._version
+        assert call(outside) is outside and outside._version > before
